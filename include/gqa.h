@@ -22,7 +22,7 @@
  *     nothing and returns a negative code, with the reason available from
  *     gqa_last_error_string() on the calling thread.
  *   - Conditions only the device can see (a seqlens entry outside [0, T_cap],
- *     a bounded wait that ran out) set bits of a device status word that
+ *     a page that a block table lacks, a bounded wait that ran out) set bits of a device status word that
  *     gqa_get_status() reads and clears.  No kernel traps.
  *   - libgqa_debug.so is the same library built with device-side index
  *     checks: before a kernel uses an index it derived (a cache row, a
@@ -67,7 +67,8 @@ enum {
     GQA_ERR_WORKSPACE = -5,   /* workspace missing or too small               */
     GQA_ERR_TIMEOUT = -6,     /* device: a bounded wait ran out               */
     GQA_ERR_SEQLEN = -7,      /* device: a seqlens entry was outside [0,T_cap] */
-    GQA_ERR_INDEX = -8        /* device, debug build only: an index check failed */
+    GQA_ERR_INDEX = -8,       /* device, debug build only: an index check failed */
+    GQA_ERR_PAGES = -9        /* device: a block table, reference count or page pool could not serve */
 };
 
 /*
@@ -337,8 +338,134 @@ GQA_API int gqa_layer_decode_step(const void *h, const void *W_Q, const void *W_
                                   size_t workspace_bytes, gqa_stream_t stream);
 
 /*
+ * gqa_prefill_packed -- causal attention over prompts of different lengths
+ * packed into one token axis: sequence b is positions cu_seqlens[b] to
+ * cu_seqlens[b+1] - 1, and for each of them and each query head i
+ *     out[s,i,:] = sum_{cu_seqlens[b] <= t <= s} softmax_t(scale <q[s,i], k[t,g]>) v[t,g,:]
+ * (section 3's causal attention, per sequence; no padding between sequences).
+ * window > 0: s - window < t <= s only; 0: no window.
+ *   q, out      device, [N, H, d_h]; k, v device, [N, G, d_h]; bf16, 16-byte
+ *               aligned; out must not overlap an input
+ *   cu_seqlens  device, [B+1] int32, 0 <= cu_seqlens[b] <= cu_seqlens[b+1] <= N;
+ *               empty sequences are allowed.  Entries out of range or falling
+ *               are clamped and flag GQA_ERR_SEQLEN.
+ * Rows of out that belong to no sequence are left as they were, and no
+ * sequence's result depends on another's values, or on those of such rows.
+ * Supported: bf16, d_h 64 or 128, H/G <= 128, B <= 8192, N*H < 2^31; scale
+ * finite and positive.
+ */
+GQA_API int gqa_prefill_packed(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, void *out,
+                               int B, int N, int H, int G, int d_h, float scale, int window, gqa_dtype dt,
+                               gqa_stream_t stream);
+
+/*
+ * Paged caches.  A paged cache is two pools k_pages, v_pages [P, G, page, d_h]
+ * and a block table [B, M] int32: entry k of row b names the page that holds
+ * positions [k page, (k+1) page) of sequence b, -1 for none.  The calls below
+ * that take `block_table` also take NULL for it: the cache is then the dense
+ * [B, G, T_cap, d_h] one of gqa_decode, and `page`, `num_pages` and `M` mean
+ * T_cap, B and 1.  A sequence's capacity is M * page positions (dense: T_cap).
+ * Reference counts [P] int32 say how many table rows list a page; 0 is free.
+ * An entry outside [0, num_pages) is never followed; where a call needs one it
+ * flags GQA_ERR_PAGES.
+ *
+ * gqa_decode_tree -- attention of a tree of drafted tokens over a cache.
+ * Sequence b has T_b = seqlens[b] cached positions, followed in the cache by the
+ * keys and values of its n_draft[b] drafts.  Draft i (query rows q[b,i,:,:]) sees
+ * every cached position, and draft j < n_draft[b] if bit j of tree_mask[b,i] is
+ * set (its ancestors and itself):
+ *     out[b,i,h,:] = sum_t softmax_t(scale <q[b,i,h], K[b,g,t]>) V[b,g,t,:]
+ * over those t.  With one draft this is a single-token step over pages.
+ *   q, out      device, [B, n, H, d_h] bf16, 16-byte aligned, not overlapping
+ *   k_cache, v_cache  device, pools or dense caches, bf16, 16-byte aligned
+ *   seqlens     device, [B] int32; T_b + n_draft[b] must not exceed the capacity
+ *   tree_mask   device, [B, n] int64 bit masks, or NULL: draft i sees drafts j <= i
+ *   n_draft     device, [B] int32, 0 <= n_draft[b] <= n, or NULL: n for all
+ *   workspace   >= gqa_decode_tree_workspace_bytes(...), 256-byte aligned; its
+ *               contents need no initialisation and nothing in it is kept
+ * Rows out[b, i >= n_draft[b]] are left as they were.  A row that sees nothing
+ * is zero.  Positions past T_b + n_draft[b] are never used, whatever they hold.
+ * A missing page counts as zeros and flags GQA_ERR_PAGES; lengths and counts out
+ * of range are clamped and flag GQA_ERR_SEQLEN.
+ * Supported: bf16, d_h 64 or 128, 1 <= n <= 64, H/G <= 128, B <= 8192, page a
+ * multiple of 16 (dense: any T_cap); scale finite and positive.
+ */
+GQA_API size_t gqa_decode_tree_workspace_bytes(int B, int n, int H, int G, int d_h);
+GQA_API int gqa_decode_tree(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                            const int32_t *seqlens, const int64_t *tree_mask, const int32_t *n_draft, float scale,
+                            void *out, int B, int n, int H, int G, int d_h, int page, int num_pages, int M,
+                            gqa_dtype dt, void *workspace, size_t workspace_bytes, gqa_stream_t stream);
+
+/*
+ * gqa_cache_append -- writes new tokens' keys and values into a cache: rows
+ * cu_seqlens[b] .. cu_seqlens[b+1] - 1 of k_new, v_new [N, G, d_h] go to
+ * positions seqlens[b], seqlens[b] + 1, ... of sequence b, and seqlens_out[b] =
+ * seqlens[b] + their number.  A sequence without room for all its rows (or with
+ * a bad range) gets none, keeps its length and flags GQA_ERR_SEQLEN; rows whose
+ * page is missing are not written and flag GQA_ERR_PAGES.  Pages of several
+ * rows must be made their own first (gqa_pages_reserve).
+ * seqlens_out must not overlap seqlens.  bf16 or fp32, d_h 64 or 128, any page.
+ */
+GQA_API int gqa_cache_append(const void *k_new, const void *v_new, const int32_t *cu_seqlens, const int32_t *seqlens,
+                             int32_t *seqlens_out, void *k_cache, void *v_cache, const int32_t *block_table, int B,
+                             int N, int G, int d_h, int page, int num_pages, int M, gqa_dtype dt,
+                             gqa_stream_t stream);
+
+/*
+ * gqa_cache_compact -- keeps some of the drafted rows behind a cache's end (the
+ * accepted path of a tree): row seqlens[b] + keep[b,j] moves to position
+ * seqlens[b] + j for j < n_keep[b], in K and V of every KV head, and
+ * seqlens_out[b] = seqlens[b] + n_keep[b].  All rows are taken as they were
+ * before the call, so any order and repetition of `keep` [B, m] int32 works.
+ * Entries lie in [0, 64); n_keep [B] int32 in [0, m], or NULL: m for all.  A
+ * sequence with an entry, count or position out of range (GQA_ERR_SEQLEN) or a
+ * page missing (GQA_ERR_PAGES) is left as it was.  1 <= m <= 64.  seqlens_out
+ * must not overlap seqlens.  bf16 or fp32, d_h 64 or 128, any page.
+ */
+GQA_API int gqa_cache_compact(void *k_cache, void *v_cache, const int32_t *block_table, const int32_t *seqlens,
+                              const int32_t *keep, const int32_t *n_keep, int32_t *seqlens_out, int B, int m, int G,
+                              int d_h, int page, int num_pages, int M, gqa_dtype dt, gqa_stream_t stream);
+
+/*
+ * gqa_pages_reserve -- makes positions [seqlens[b], seqlens[b] + n_new[b]) of
+ * every sequence writable by it alone.  A missing entry there gets a free page;
+ * a page that other rows share is replaced by a free one (copy-on-write: the
+ * rows below seqlens[b] are copied, the shared page loses a reference).  Which
+ * entries need a page is decided on the counts before the call, and the lowest
+ * free pages are handed out in table order, so the result is deterministic.
+ * All or nothing: with too few free pages nothing changes and GQA_ERR_PAGES is
+ * flagged.  A sequence whose range is negative or beyond its capacity is
+ * skipped and flags GQA_ERR_SEQLEN.
+ *   workspace >= gqa_pages_reserve_workspace_bytes(B, num_pages), 256-byte aligned
+ */
+GQA_API size_t gqa_pages_reserve_workspace_bytes(int B, int num_pages);
+GQA_API int gqa_pages_reserve(int32_t *block_table, int32_t *refcount, const int32_t *seqlens, const int32_t *n_new,
+                              void *k_pages, void *v_pages, int B, int G, int d_h, int page, int num_pages, int M,
+                              gqa_dtype dt, void *workspace, size_t workspace_bytes, gqa_stream_t stream);
+
+/*
+ * gqa_pages_fork -- sequence dst[i] becomes a copy of sequence src[i] (beams,
+ * shared prompts): its empty table row lists the same pages up to
+ * seqlens[src[i]], each with one more reference, and seqlens[dst[i]] =
+ * seqlens[src[i]].  Nothing is copied until gqa_pages_reserve.  A pair is
+ * skipped and flags GQA_ERR_PAGES when an index is outside [0, B), a dst row is
+ * not empty, is some pair's src or is an earlier pair's dst, or src lacks a page.
+ */
+GQA_API int gqa_pages_fork(int32_t *block_table, int32_t *refcount, int32_t *seqlens, const int32_t *src,
+                           const int32_t *dst, int n, int B, int page, int num_pages, int M, gqa_stream_t stream);
+
+/*
+ * gqa_pages_release -- gives back the pages that lengths[b] positions do not
+ * need (0: all of them): those entries become -1 and their pages lose a
+ * reference.  An entry out of range or of a page without references flags
+ * GQA_ERR_PAGES, a negative length GQA_ERR_SEQLEN (the row is then left alone).
+ */
+GQA_API int gqa_pages_release(int32_t *block_table, int32_t *refcount, const int32_t *lengths, int B, int page,
+                              int num_pages, int M, gqa_stream_t stream);
+
+/*
  * gqa_get_status -- synchronises `stream`, then reads and clears the device
- * status word: GQA_OK, GQA_ERR_SEQLEN, GQA_ERR_TIMEOUT or (debug build)
+ * status word: GQA_OK, GQA_ERR_SEQLEN, GQA_ERR_PAGES, GQA_ERR_TIMEOUT or (debug build)
  * GQA_ERR_INDEX (device-side conditions of earlier calls on this device; the
  * most severe is returned), or GQA_ERR_CUDA if the synchronisation itself
  * failed.

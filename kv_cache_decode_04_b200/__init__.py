@@ -10,6 +10,10 @@ Calls (same names as the C ABI, without the ``gqa_`` prefix):
 
 * :func:`decode` -- one decode step over a [B, G, T_cap, d_h] KV cache.
 * :func:`prefill_causal` -- causal attention over a whole prompt.
+* :func:`prefill_packed` -- the same over prompts of different lengths, packed.
+* :func:`decode_tree` -- a tree of drafted tokens over a dense or paged cache.
+* :func:`cache_append`, :func:`cache_compact` -- rows into a cache; the accepted ones kept.
+* :func:`pages_reserve`, :func:`pages_fork`, :func:`pages_release` -- a pool of cache pages.
 * :func:`meanpool_kv` -- averaging-init of G K/V heads from H MHA heads.
 * :func:`kv_cache_bytes` -- KV-cache bytes per token, 2*G*d_h*L*elem_bytes.
 * :func:`get_status` -- device-side status of earlier calls.
@@ -24,6 +28,8 @@ import torch
 
 __all__ = ["decode", "decode_noalloc", "decode_workspace_bytes", "prefill_causal", "meanpool_kv",
            "qkv_append", "init_kv_heads", "out_project", "project_workspace_bytes", "layer_decode_step",
+           "prefill_packed", "decode_tree", "decode_tree_workspace_bytes", "cache_append", "cache_compact",
+           "pages_reserve", "pages_fork", "pages_release",
            "kv_cache_bytes", "get_status", "GQAError", "LIB_PATH", "lib"]
 
 # GQA_LIB=debug selects libgqa_debug.so: the same kernels with device-side
@@ -33,7 +39,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
 
 GQA_F32, GQA_BF16 = 0, 1
 _ERRORS = {-1: "INVALID", -2: "UNSUPPORTED", -3: "ALIGN", -4: "CUDA", -5: "WORKSPACE",
-           -6: "TIMEOUT", -7: "SEQLEN", -8: "INDEX"}
+           -6: "TIMEOUT", -7: "SEQLEN", -8: "INDEX", -9: "PAGES"}
 
 # Every symbol include/gqa.h declares.
 EXPORTS = ("gqa_kv_cache_bytes", "gqa_decode_workspace_bytes", "gqa_decode",
@@ -41,6 +47,9 @@ EXPORTS = ("gqa_kv_cache_bytes", "gqa_decode_workspace_bytes", "gqa_decode",
            "gqa_prefill_causal_window", "gqa_meanpool_kv", "gqa_init_kv_heads", "gqa_qkv_append",
            "gqa_out_project", "gqa_project_workspace_bytes", "gqa_layer_decode_workspace_bytes",
            "gqa_layer_decode_step",
+           "gqa_prefill_packed", "gqa_decode_tree", "gqa_decode_tree_workspace_bytes", "gqa_cache_append",
+           "gqa_cache_compact", "gqa_pages_reserve", "gqa_pages_reserve_workspace_bytes", "gqa_pages_fork",
+           "gqa_pages_release",
            "gqa_selftest_wait_timeout", "gqa_get_status", "gqa_last_error_string", "gqa_version")
 
 
@@ -90,6 +99,25 @@ def _load():
     L.gqa_layer_decode_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, f32, i32, vp, i32, i32,
                                         i32, i32, i32, i32, i32, vp, sz, vp]
     L.gqa_layer_decode_step.restype = i32
+    L.gqa_prefill_packed.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, i32, i32, vp]
+    L.gqa_prefill_packed.restype = i32
+    L.gqa_decode_tree_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.gqa_decode_tree_workspace_bytes.restype = sz
+    L.gqa_decode_tree.argtypes = [vp, vp, vp, vp, vp, vp, vp, f32, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32,
+                                  vp, sz, vp]
+    L.gqa_decode_tree.restype = i32
+    L.gqa_cache_append.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp]
+    L.gqa_cache_append.restype = i32
+    L.gqa_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp]
+    L.gqa_cache_compact.restype = i32
+    L.gqa_pages_reserve_workspace_bytes.argtypes = [i32, i32]
+    L.gqa_pages_reserve_workspace_bytes.restype = sz
+    L.gqa_pages_reserve.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, sz, vp]
+    L.gqa_pages_reserve.restype = i32
+    L.gqa_pages_fork.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]
+    L.gqa_pages_fork.restype = i32
+    L.gqa_pages_release.argtypes = [vp, vp, vp, i32, i32, i32, i32, vp]
+    L.gqa_pages_release.restype = i32
     L.gqa_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp, vp]
     L.gqa_selftest_wait_timeout.restype = i32
     L.gqa_get_status.argtypes = [vp]
@@ -353,6 +381,236 @@ def layer_decode_step(h, W_Q, W_K, W_V, W_O, k_cache, v_cache, seqlens, scale=No
                                    _dev(workspace, "workspace"), workspace.numel(), _stream(stream))
     _check(rc)
     return out, seqlens_out
+
+
+# ---------------------------------------------------------------- packed prompts, paged caches
+
+
+def _same(what, device, *named):
+    """Every tensor is a contiguous CUDA tensor on `device`, the current one."""
+    for name, t in named:
+        if t.device != device:
+            raise ValueError("%s is on %s, %s on %s" % (name, t.device, what, device))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    if device.type != "cuda":
+        raise TypeError("%s must be a CUDA tensor" % what)
+    if device.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, which is not the current device" % (what, device))
+
+
+def _int32(name, t, *shape):
+    if t.dtype != torch.int32 or t.shape != shape:
+        raise ValueError("%s must be int32 %s" % (name, list(shape)))
+
+
+def _empty(stream, *size, dtype, device):
+    """torch.empty whose memory belongs to `stream` (None: the current stream), so that the
+    allocator does not hand it on while a kernel queued there still uses it."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=dtype, device=device)
+
+
+def _cache(k_cache, v_cache, block_table, B):
+    """(table pointer, G, page, num_pages, M) of a paged cache, or of a dense one without a table."""
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must share a 4-d shape and a dtype")
+    P, G, page, _ = k_cache.shape
+    if block_table is None:
+        if P != B:
+            raise ValueError("a dense cache must be [B, G, T_cap, d_h] with B = %d" % B)
+        return None, G, page, P, 1
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be int32 [B, M] with B = %d" % B)
+    return block_table.data_ptr(), G, page, P, block_table.shape[1]
+
+
+def _tensors(**named):
+    return [(n, t) for n, t in named.items() if t is not None]
+
+
+def prefill_packed(q, k, v, cu_seqlens, scale=None, out=None, stream=None, window=0):
+    """Causal GQA prefill of prompts of different lengths packed into one token axis.
+
+    q [N,H,d_h], k/v [N,G,d_h] bf16; cu_seqlens [B+1] int32 (device): sequence b is positions
+    cu_seqlens[b] to cu_seqlens[b+1] - 1.  window > 0: position s sees s-window < t <= s only.
+    Rows of ``out`` that belong to no sequence are left as they were.
+    """
+    N, H, d_h = q.shape
+    G = k.shape[1] if k.dim() == 3 else 0
+    if k.shape != (N, G, d_h) or v.shape != k.shape:
+        raise ValueError("shape mismatch between q, k and v")
+    if q.dtype != k.dtype or q.dtype != v.dtype:
+        raise TypeError("q, k and v must share a dtype")
+    code = _dtype_code(q)
+    B = cu_seqlens.numel() - 1
+    _int32("cu_seqlens", cu_seqlens, B + 1)
+    if out is None:
+        out = _empty(stream, N, H, d_h, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    _same("q", q.device, ("q", q), ("k", k), ("v", v), ("cu_seqlens", cu_seqlens), ("out", out))
+    _check(lib.gqa_prefill_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), out.data_ptr(), B,
+                                  N, H, G, d_h, 1.0 / math.sqrt(d_h) if scale is None else float(scale), int(window),
+                                  code, _stream(stream)))
+    return out
+
+
+def decode_tree_workspace_bytes(B, n, H, G, d_h) -> int:
+    size = int(lib.gqa_decode_tree_workspace_bytes(B, n, H, G, d_h))
+    if size == 0:
+        raise GQAError(-1, "invalid draft shape or device: " + lib.gqa_last_error_string().decode())
+    return size
+
+
+def decode_tree(q, k_cache, v_cache, seqlens, tree_mask=None, n_draft=None, block_table=None, scale=None, out=None,
+                workspace=None, stream=None):
+    """Attention of drafted tokens over a cache: q [B,n,H,d_h] -> out [B,n,H,d_h], bf16.
+
+    Sequence b holds seqlens[b] positions, followed by its n_draft[b] (None: n) drafts' K/V.
+    Draft i sees every cached position and the drafts j whose bit j is set in tree_mask[b,i]
+    (int64 [B,n]; None: drafts j <= i).  block_table [B,M] int32 names the pages of k_cache and
+    v_cache [P,G,page,d_h]; None: dense caches [B,G,T_cap,d_h].  Rows of ``out`` past n_draft[b]
+    are left as they were.
+    """
+    B, n, H, d_h = q.shape
+    table, G, page, P, M = _cache(k_cache, v_cache, block_table, B)
+    if k_cache.shape[3] != d_h:
+        raise ValueError("q and the caches disagree on d_h")
+    if q.dtype != k_cache.dtype:
+        raise TypeError("q, k_cache and v_cache must share a dtype")
+    code = _dtype_code(q)
+    _int32("seqlens", seqlens, B)
+    if tree_mask is not None and (tree_mask.dtype != torch.int64 or tree_mask.shape != (B, n)):
+        raise ValueError("tree_mask must be int64 [B, n]")
+    if n_draft is not None:
+        _int32("n_draft", n_draft, B)
+    if out is None:
+        out = _empty(stream, B, n, H, d_h, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and dtype")
+    if workspace is None:
+        workspace = _empty(stream, decode_tree_workspace_bytes(B, n, H, G, d_h), dtype=torch.uint8, device=q.device)
+    _same("q", q.device, *_tensors(q=q, k_cache=k_cache, v_cache=v_cache, seqlens=seqlens, tree_mask=tree_mask,
+                                   n_draft=n_draft, block_table=block_table, out=out, workspace=workspace))
+    _check(lib.gqa_decode_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, seqlens.data_ptr(),
+                               None if tree_mask is None else tree_mask.data_ptr(),
+                               None if n_draft is None else n_draft.data_ptr(),
+                               1.0 / math.sqrt(d_h) if scale is None else float(scale), out.data_ptr(), B, n, H, G,
+                               d_h, page, P, M, code, workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
+
+
+def cache_append(k_new, v_new, cu_seqlens, seqlens, k_cache, v_cache, block_table=None, seqlens_out=None, stream=None):
+    """Writes packed new rows k_new, v_new [N,G,d_h] into a cache: rows cu_seqlens[b] to
+    cu_seqlens[b+1] - 1 go to positions seqlens[b], seqlens[b] + 1, ... of sequence b.
+
+    Returns seqlens_out [B] = seqlens + the rows of each.  block_table None: dense caches.
+    """
+    B = seqlens.numel()
+    table, G, page, P, M = _cache(k_cache, v_cache, block_table, B)
+    d_h = k_cache.shape[3]
+    N = k_new.shape[0]
+    if k_new.shape != (N, G, d_h) or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [N, G, d_h] of the caches' G and d_h")
+    if k_new.dtype != k_cache.dtype or v_new.dtype != k_cache.dtype:
+        raise TypeError("the new rows and the caches must share a dtype")
+    code = _dtype_code(k_cache)
+    _int32("seqlens", seqlens, B)
+    _int32("cu_seqlens", cu_seqlens, B + 1)
+    if seqlens_out is None:
+        seqlens_out = _empty(stream, B, dtype=torch.int32, device=k_cache.device)
+    else:
+        _int32("seqlens_out", seqlens_out, B)
+    _same("k_cache", k_cache.device, *_tensors(k_cache=k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new,
+                                               cu_seqlens=cu_seqlens, seqlens=seqlens, seqlens_out=seqlens_out,
+                                               block_table=block_table))
+    _check(lib.gqa_cache_append(k_new.data_ptr(), v_new.data_ptr(), cu_seqlens.data_ptr(), seqlens.data_ptr(),
+                                seqlens_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, B, N, G, d_h,
+                                page, P, M, code, _stream(stream)))
+    return seqlens_out
+
+
+def cache_compact(k_cache, v_cache, seqlens, keep, n_keep=None, block_table=None, seqlens_out=None, stream=None):
+    """Keeps drafted rows (the accepted path): row seqlens[b] + keep[b,j] moves to position
+    seqlens[b] + j for j < n_keep[b] (None: all m of keep [B,m] int32, entries in [0, 64)).
+
+    Returns seqlens_out [B] = seqlens + n_keep.  block_table None: dense caches.
+    """
+    B = seqlens.numel()
+    table, G, page, P, M = _cache(k_cache, v_cache, block_table, B)
+    code = _dtype_code(k_cache)
+    _int32("seqlens", seqlens, B)
+    m = keep.shape[1] if keep.dim() == 2 else 0
+    _int32("keep", keep, B, m)
+    if n_keep is not None:
+        _int32("n_keep", n_keep, B)
+    if seqlens_out is None:
+        seqlens_out = _empty(stream, B, dtype=torch.int32, device=k_cache.device)
+    else:
+        _int32("seqlens_out", seqlens_out, B)
+    _same("k_cache", k_cache.device, *_tensors(k_cache=k_cache, v_cache=v_cache, seqlens=seqlens, keep=keep,
+                                               n_keep=n_keep, seqlens_out=seqlens_out, block_table=block_table))
+    _check(lib.gqa_cache_compact(k_cache.data_ptr(), v_cache.data_ptr(), table, seqlens.data_ptr(), keep.data_ptr(),
+                                 None if n_keep is None else n_keep.data_ptr(), seqlens_out.data_ptr(), B, m, G,
+                                 k_cache.shape[3], page, P, M, code, _stream(stream)))
+    return seqlens_out
+
+
+def _pool(block_table, refcount):
+    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [B, M]")
+    if refcount.dtype != torch.int32 or refcount.dim() != 1:
+        raise ValueError("refcount must be int32 [P]")
+    return block_table.shape[0], block_table.shape[1], refcount.shape[0]
+
+
+def pages_reserve(block_table, refcount, seqlens, n_new, k_pages, v_pages, workspace=None, stream=None):
+    """Makes positions [seqlens[b], seqlens[b] + n_new[b]) of every sequence its own: missing pages are
+    taken from the pool (lowest free page first, in table order), shared ones are replaced by a copy.
+    block_table [B,M] and refcount [P] int32 are updated in place.  All or nothing."""
+    B, M, P = _pool(block_table, refcount)
+    _, G, page, _, _ = _cache(k_pages, v_pages, block_table, B)
+    if k_pages.shape[0] != P:
+        raise ValueError("refcount must hold one count per page (%d)" % k_pages.shape[0])
+    code = _dtype_code(k_pages)
+    _int32("seqlens", seqlens, B)
+    _int32("n_new", n_new, B)
+    if workspace is None:
+        workspace = _empty(stream, int(lib.gqa_pages_reserve_workspace_bytes(B, P)), dtype=torch.uint8,
+                           device=k_pages.device)
+    _same("k_pages", k_pages.device, *_tensors(k_pages=k_pages, v_pages=v_pages, block_table=block_table,
+                                               refcount=refcount, seqlens=seqlens, n_new=n_new, workspace=workspace))
+    _check(lib.gqa_pages_reserve(block_table.data_ptr(), refcount.data_ptr(), seqlens.data_ptr(), n_new.data_ptr(),
+                                 k_pages.data_ptr(), v_pages.data_ptr(), B, G, k_pages.shape[3], page, P, M, code,
+                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def pages_fork(block_table, refcount, seqlens, src, dst, page_size, stream=None):
+    """Sequence dst[i] becomes a copy of src[i] that shares its pages (block_table, refcount and seqlens are
+    updated in place).  dst rows must be empty; the pages are copied when pages_reserve needs them apart."""
+    B, M, P = _pool(block_table, refcount)
+    _int32("seqlens", seqlens, B)
+    n = src.numel()
+    _int32("src", src, n)
+    _int32("dst", dst, n)
+    _same("block_table", block_table.device, ("block_table", block_table), ("refcount", refcount),
+          ("seqlens", seqlens), ("src", src), ("dst", dst))
+    _check(lib.gqa_pages_fork(block_table.data_ptr(), refcount.data_ptr(), seqlens.data_ptr(), src.data_ptr(),
+                              dst.data_ptr(), n, B, int(page_size), P, M, _stream(stream)))
+
+
+def pages_release(block_table, refcount, lengths, page_size, stream=None):
+    """Gives back the pages that lengths[b] positions of each sequence do not need (0: all of them)."""
+    B, M, P = _pool(block_table, refcount)
+    _int32("lengths", lengths, B)
+    _same("block_table", block_table.device, ("block_table", block_table), ("refcount", refcount),
+          ("lengths", lengths))
+    _check(lib.gqa_pages_release(block_table.data_ptr(), refcount.data_ptr(), lengths.data_ptr(), B, int(page_size),
+                                 P, M, _stream(stream)))
 
 
 def get_status(stream=None):

@@ -565,6 +565,329 @@ int gqa_layer_decode_step(const void *h, const void *W_Q, const void *W_K, const
     return gqa_out_project(attn, W_O, out, B, H * d_h, d, dt, pws, pbytes, stream);
 }
 
+static bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
+    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+    return x < y + nb && y < x + na;
+}
+
+// Packed query rows [N, H, d_h]: boxes of 64 dims x the r heads of a group x
+// floor(128 / r) tokens, the rows of one tensor-core tile.
+static int make_tmap_rows(CUtensorMap *m, const void *q, long long N, int H, int G, int d_h) {
+    const int r = H / G;
+    const cuuint64_t dims[3] = {(cuuint64_t)d_h, (cuuint64_t)H, (cuuint64_t)N};
+    const cuuint64_t strides[2] = {(cuuint64_t)d_h * 2, (cuuint64_t)H * d_h * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)r, (cuuint32_t)(128 / r)};
+    return make_tmap_bf16(m, q, 3, dims, strides, box);
+}
+
+int gqa_prefill_packed(const void *q, const void *k, const void *v, const int32_t *cu_seqlens, void *out, int B, int N,
+                       int H, int G, int d_h, float scale, int window, gqa_dtype dt, gqa_stream_t stream) {
+    t_err[0] = 0;
+    int rc = check_dims(B, H, G, d_h);
+    if (rc) return rc;
+    if (window < 0) return fail(GQA_ERR_INVALID, "window must be >= 0 (0: no window)");
+    if (N <= 0) return fail(GQA_ERR_INVALID, "N must be positive");
+    if (!q || !k || !v || !cu_seqlens || !out) return fail(GQA_ERR_INVALID, "null tensor pointer");
+    if (!std::isfinite(scale) || !(scale > 0.f))
+        return fail(GQA_ERR_INVALID, "prefill scale must be finite and positive");
+    if (dt != GQA_BF16) return fail(GQA_ERR_UNSUPPORTED, "prefill supports bf16 only");
+    if (d_h != 64 && d_h != 128) return fail(GQA_ERR_UNSUPPORTED, "prefill d_h=%d (built: 64, 128)", d_h);
+    if (H / G > 128) return fail(GQA_ERR_UNSUPPORTED, "packed prefill needs H/G <= 128 (got %d)", H / G);
+    if (B > 8192) return fail(GQA_ERR_UNSUPPORTED, "B=%d above 8192", B);
+    if ((long long)N * H >= (1ll << 31)) return fail(GQA_ERR_UNSUPPORTED, "N*H must be below 2^31");
+    if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(out, 16) || misaligned(cu_seqlens, 4))
+        return fail(GQA_ERR_ALIGN, "q, k, v and out must be 16-byte aligned");
+    const size_t qb = (size_t)N * H * d_h * 2, kb = (size_t)N * G * d_h * 2;
+    if (overlaps(out, qb, q, qb) || overlaps(out, qb, k, kb) || overlaps(out, qb, v, kb) ||
+        overlaps(out, qb, cu_seqlens, (size_t)(B + 1) * 4))
+        return fail(GQA_ERR_INVALID, "out must not overlap an input");
+    DeviceInfo *d = nullptr;
+    rc = device_info(&d);
+    if (rc) return rc;
+    CUtensorMap tmq, tmk, tmv;
+    rc = make_tmap_rows(&tmq, q, N, H, G, d_h);
+    if (rc) return rc;
+    {
+        const cuuint64_t dims[3] = {(cuuint64_t)d_h, (cuuint64_t)G, (cuuint64_t)N};
+        const cuuint64_t strides[2] = {(cuuint64_t)d_h * 2, (cuuint64_t)G * d_h * 2};
+        const cuuint32_t box[3] = {64, 1, 128};
+        rc = make_tmap_bf16(&tmk, k, 3, dims, strides, box);
+        if (rc) return rc;
+        rc = make_tmap_bf16(&tmv, v, 3, dims, strides, box);
+        if (rc) return rc;
+    }
+    gqa::PackedArgs a = {};
+    a.cu = cu_seqlens;
+    a.out = out;
+    a.scale = scale;
+    a.B = B;
+    a.N = N;
+    a.H = H;
+    a.G = G;
+    a.d_h = d_h;
+    a.status = d->status;
+    a.timeout_ns = wait_timeout_ns();
+    a.window = window;
+    cudaError_t e = gqa::launch_prefill_packed(a, &tmq, &tmk, &tmv, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail_cuda(e, "packed prefill launch");
+    return GQA_OK;
+}
+
+// Checks a dense or paged cache's description and fills the kernels' view of it.
+static int cache_view(gqa::CacheView *c, const int32_t *table, int B, int G, int d_h, int page, int num_pages, int M,
+                      gqa_dtype dt) {
+    if (B <= 0 || G <= 0 || page <= 0 || num_pages <= 0 || M <= 0)
+        return fail(GQA_ERR_INVALID, "cache dimensions must be positive (B=%d G=%d page=%d num_pages=%d M=%d)", B, G,
+                    page, num_pages, M);
+    if (dt != GQA_BF16 && dt != GQA_F32) return fail(GQA_ERR_UNSUPPORTED, "dtype %d", (int)dt);
+    if (d_h != 64 && d_h != 128) return fail(GQA_ERR_UNSUPPORTED, "d_h=%d (built: 64, 128)", d_h);
+    if (B > 8192) return fail(GQA_ERR_UNSUPPORTED, "B=%d above 8192", B);
+    if (!table && (num_pages != B || M != 1))
+        return fail(GQA_ERR_INVALID, "a dense cache (no block table) has num_pages = B and M = 1");
+    if ((long long)M * page > INT32_MAX - 256)
+        return fail(GQA_ERR_UNSUPPORTED, "a sequence's capacity must stay below 2^31 positions");
+    if ((long long)num_pages * G * page >= (1ll << 40) / d_h) return fail(GQA_ERR_UNSUPPORTED, "cache too large");
+    if (misaligned(table, 4)) return fail(GQA_ERR_ALIGN, "block_table must be 4-byte aligned");
+    c->table = table;
+    c->B = B;
+    c->G = G;
+    c->M = M;
+    c->page = page;
+    c->num_pages = num_pages;
+    c->cap = M * page;
+    c->row16 = d_h * (dt == GQA_BF16 ? 2 : 4) / 16;
+    return GQA_OK;
+}
+
+static size_t cache_bytes(const gqa::CacheView &c) { return (size_t)c.num_pages * c.G * c.page * c.row16 * 16; }
+
+size_t gqa_decode_tree_workspace_bytes(int B, int n, int H, int G, int d_h) {
+    if (check_dims(B, H, G, d_h)) return 0;
+    if (n <= 0 || n > 64 || H / G > 128 || (d_h != 64 && d_h != 128)) {
+        fail(GQA_ERR_UNSUPPORTED, "unsupported draft shape (n=%d H/G=%d d_h=%d)", n, H / G, d_h);
+        return 0;
+    }
+    DeviceInfo *d = nullptr;
+    if (device_info(&d)) return 0;
+    return gqa::decode_tree_workspace(B, n, H / G, d_h, d->num_sms);
+}
+
+int gqa_decode_tree(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
+                    const int32_t *seqlens, const int64_t *tree_mask, const int32_t *n_draft, float scale, void *out,
+                    int B, int n, int H, int G, int d_h, int page, int num_pages, int M, gqa_dtype dt, void *workspace,
+                    size_t workspace_bytes, gqa_stream_t stream) {
+    t_err[0] = 0;
+    int rc = check_dims(B, H, G, d_h);
+    if (rc) return rc;
+    if (n <= 0 || n > 64) return fail(GQA_ERR_INVALID, "n=%d drafts (1 to 64)", n);
+    if (!q || !k_cache || !v_cache || !seqlens || !out) return fail(GQA_ERR_INVALID, "null tensor pointer");
+    if (!std::isfinite(scale) || !(scale > 0.f))
+        return fail(GQA_ERR_INVALID, "tree decode scale must be finite and positive");
+    if (dt != GQA_BF16) return fail(GQA_ERR_UNSUPPORTED, "tree decode supports bf16 only");
+    const int r = H / G;
+    if (r > 128) return fail(GQA_ERR_UNSUPPORTED, "tree decode needs H/G <= 128 (got %d)", r);
+    gqa::CacheView c = {};
+    rc = cache_view(&c, block_table, B, G, d_h, page, num_pages, M, dt);
+    if (rc) return rc;
+    if (block_table && page % 16) return fail(GQA_ERR_UNSUPPORTED, "page=%d must be a multiple of 16", page);
+    const long long pt = 128 / r, blocks = (n + pt - 1) / pt;
+    if ((long long)B * G * blocks * ((c.cap + 127ll) / 128) >= (1ll << 31) || (long long)B * n * H >= (1ll << 31))
+        return fail(GQA_ERR_UNSUPPORTED, "too many key tiles or query rows for one call");
+    if (misaligned(q, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(out, 16) ||
+        misaligned(seqlens, 4) || misaligned(tree_mask, 8) || misaligned(n_draft, 4))
+        return fail(GQA_ERR_ALIGN, "q, k_cache, v_cache and out must be 16-byte aligned, tree_mask 8-byte");
+    const size_t qb = (size_t)B * n * H * d_h * 2, cb = cache_bytes(c);
+    if (overlaps(out, qb, q, qb) || overlaps(out, qb, k_cache, cb) || overlaps(out, qb, v_cache, cb))
+        return fail(GQA_ERR_INVALID, "out must not overlap an input");
+    DeviceInfo *d = nullptr;
+    rc = device_info(&d);
+    if (rc) return rc;
+    const size_t need = gqa::decode_tree_workspace(B, n, r, d_h, d->num_sms);
+    if (!workspace || workspace_bytes < need)
+        return fail(GQA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                    workspace ? workspace_bytes : (size_t)0);
+    if (misaligned(workspace, 256)) return fail(GQA_ERR_ALIGN, "workspace must be 256-byte aligned");
+    // one K/V load is the largest power of two that divides the page, 128 at most; a
+    // dense row is one page, and what a load takes beyond it reads as zero
+    int box = 128;
+    if (block_table)
+        while (page % box) box /= 2;
+    CUtensorMap tmq, tmk, tmv;
+    rc = make_tmap_rows(&tmq, q, (long long)B * n, H, G, d_h);
+    if (rc) return rc;
+    {
+        const cuuint64_t dims[4] = {(cuuint64_t)d_h, (cuuint64_t)page, (cuuint64_t)G, (cuuint64_t)num_pages};
+        const cuuint64_t strides[3] = {(cuuint64_t)d_h * 2, (cuuint64_t)page * d_h * 2,
+                                       (cuuint64_t)G * page * d_h * 2};
+        const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1};
+        rc = make_tmap_bf16(&tmk, k_cache, 4, dims, strides, boxes);
+        if (rc) return rc;
+        rc = make_tmap_bf16(&tmv, v_cache, 4, dims, strides, boxes);
+        if (rc) return rc;
+    }
+    gqa::TreeArgs a = {};
+    a.seqlens = seqlens;
+    a.mask = tree_mask;
+    a.n_draft = n_draft;
+    a.out = out;
+    a.scale = scale;
+    a.n = n;
+    a.H = H;
+    a.d_h = d_h;
+    a.box = box;
+    a.cache = c;
+    a.workspace = workspace;
+    a.status = d->status;
+    a.timeout_ns = wait_timeout_ns();
+    a.num_sms = d->num_sms;
+    cudaError_t e = gqa::launch_decode_tree(a, &tmq, &tmk, &tmv, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail_cuda(e, "tree decode launch");
+    return GQA_OK;
+}
+
+int gqa_cache_append(const void *k_new, const void *v_new, const int32_t *cu_seqlens, const int32_t *seqlens,
+                     int32_t *seqlens_out, void *k_cache, void *v_cache, const int32_t *block_table, int B, int N,
+                     int G, int d_h, int page, int num_pages, int M, gqa_dtype dt, gqa_stream_t stream) {
+    t_err[0] = 0;
+    gqa::CacheView c = {};
+    int rc = cache_view(&c, block_table, B, G, d_h, page, num_pages, M, dt);
+    if (rc) return rc;
+    if (N <= 0) return fail(GQA_ERR_INVALID, "N must be positive");
+    if (!k_new || !v_new || !cu_seqlens || !seqlens || !seqlens_out || !k_cache || !v_cache)
+        return fail(GQA_ERR_INVALID, "null tensor pointer");
+    if (overlaps(seqlens_out, (size_t)B * 4, seqlens, (size_t)B * 4) ||
+        overlaps(seqlens_out, (size_t)B * 4, cu_seqlens, (size_t)(B + 1) * 4))
+        return fail(GQA_ERR_INVALID, "seqlens_out must not overlap seqlens or cu_seqlens");
+    const size_t nb = (size_t)N * G * c.row16 * 16, cb = cache_bytes(c);
+    if (overlaps(k_cache, cb, v_cache, cb) || overlaps(k_cache, cb, k_new, nb) || overlaps(k_cache, cb, v_new, nb) ||
+        overlaps(v_cache, cb, k_new, nb) || overlaps(v_cache, cb, v_new, nb))
+        return fail(GQA_ERR_INVALID, "the caches must not overlap each other or the new rows");
+    if (misaligned(k_new, 16) || misaligned(v_new, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) ||
+        misaligned(cu_seqlens, 4) || misaligned(seqlens, 4) || misaligned(seqlens_out, 4))
+        return fail(GQA_ERR_ALIGN, "k_new, v_new and the caches must be 16-byte aligned");
+    DeviceInfo *d = nullptr;
+    rc = device_info(&d);
+    if (rc) return rc;
+    cudaError_t e = gqa::launch_cache_append(k_new, v_new, cu_seqlens, seqlens, seqlens_out, k_cache, v_cache, c, N,
+                                             d->num_sms, d->status, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail_cuda(e, "cache append launch");
+    return GQA_OK;
+}
+
+int gqa_cache_compact(void *k_cache, void *v_cache, const int32_t *block_table, const int32_t *seqlens,
+                      const int32_t *keep, const int32_t *n_keep, int32_t *seqlens_out, int B, int m, int G, int d_h,
+                      int page, int num_pages, int M, gqa_dtype dt, gqa_stream_t stream) {
+    t_err[0] = 0;
+    gqa::CacheView c = {};
+    int rc = cache_view(&c, block_table, B, G, d_h, page, num_pages, M, dt);
+    if (rc) return rc;
+    if (m <= 0 || m > 64) return fail(GQA_ERR_INVALID, "m=%d entries to keep (1 to 64)", m);
+    if (!k_cache || !v_cache || !seqlens || !keep || !seqlens_out)
+        return fail(GQA_ERR_INVALID, "null tensor pointer");
+    if (overlaps(seqlens_out, (size_t)B * 4, seqlens, (size_t)B * 4) ||
+        overlaps(seqlens_out, (size_t)B * 4, keep, (size_t)B * m * 4) ||
+        (n_keep && overlaps(seqlens_out, (size_t)B * 4, n_keep, (size_t)B * 4)))
+        return fail(GQA_ERR_INVALID, "seqlens_out must not overlap seqlens, keep or n_keep");
+    if (overlaps(k_cache, cache_bytes(c), v_cache, cache_bytes(c)))
+        return fail(GQA_ERR_INVALID, "the caches must not overlap each other");
+    if ((long long)B * G * 2 >= (1ll << 31)) return fail(GQA_ERR_UNSUPPORTED, "B*G too large");
+    if (misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(seqlens, 4) || misaligned(keep, 4) ||
+        misaligned(n_keep, 4) || misaligned(seqlens_out, 4))
+        return fail(GQA_ERR_ALIGN, "the caches must be 16-byte aligned");
+    DeviceInfo *d = nullptr;
+    rc = device_info(&d);
+    if (rc) return rc;
+    cudaError_t e = gqa::launch_cache_compact(k_cache, v_cache, seqlens, keep, n_keep, seqlens_out, c, m, d->status,
+                                              reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail_cuda(e, "cache compact launch");
+    return GQA_OK;
+}
+
+size_t gqa_pages_reserve_workspace_bytes(int B, int num_pages) {
+    if (B <= 0 || num_pages <= 0) return 0;
+    return gqa::pages_reserve_workspace(B, num_pages);
+}
+
+// The page pool's integer tensors: present, aligned, of sane sizes and apart.
+static int check_pool(const int32_t *table, const int32_t *refcount, int B, int page, int num_pages, int M) {
+    if (B <= 0 || page <= 0 || num_pages <= 0 || M <= 0)
+        return fail(GQA_ERR_INVALID, "pool dimensions must be positive (B=%d page=%d num_pages=%d M=%d)", B, page,
+                    num_pages, M);
+    if (B > 8192) return fail(GQA_ERR_UNSUPPORTED, "B=%d above 8192", B);
+    if (num_pages > (1 << 30) || (long long)M * page > INT32_MAX - 256)
+        return fail(GQA_ERR_UNSUPPORTED, "num_pages above 2^30 or a capacity above 2^31 positions");
+    if (!table || !refcount) return fail(GQA_ERR_INVALID, "null tensor pointer");
+    if (misaligned(table, 4) || misaligned(refcount, 4))
+        return fail(GQA_ERR_ALIGN, "block_table and refcount must be 4-byte aligned");
+    if (overlaps(table, (size_t)B * M * 4, refcount, (size_t)num_pages * 4))
+        return fail(GQA_ERR_INVALID, "block_table and refcount must not overlap");
+    return GQA_OK;
+}
+
+int gqa_pages_reserve(int32_t *block_table, int32_t *refcount, const int32_t *seqlens, const int32_t *n_new,
+                      void *k_pages, void *v_pages, int B, int G, int d_h, int page, int num_pages, int M, gqa_dtype dt,
+                      void *workspace, size_t workspace_bytes, gqa_stream_t stream) {
+    t_err[0] = 0;
+    int rc = check_pool(block_table, refcount, B, page, num_pages, M);
+    if (rc) return rc;
+    gqa::CacheView c = {};
+    rc = cache_view(&c, block_table, B, G, d_h, page, num_pages, M, dt);
+    if (rc) return rc;
+    if (!seqlens || !n_new || !k_pages || !v_pages) return fail(GQA_ERR_INVALID, "null tensor pointer");
+    if (overlaps(k_pages, cache_bytes(c), v_pages, cache_bytes(c)))
+        return fail(GQA_ERR_INVALID, "the pools must not overlap each other");
+    if (misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(seqlens, 4) || misaligned(n_new, 4))
+        return fail(GQA_ERR_ALIGN, "the pools must be 16-byte aligned");
+    const size_t need = gqa::pages_reserve_workspace(B, num_pages);
+    if (!workspace || workspace_bytes < need)
+        return fail(GQA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                    workspace ? workspace_bytes : (size_t)0);
+    if (misaligned(workspace, 256)) return fail(GQA_ERR_ALIGN, "workspace must be 256-byte aligned");
+    DeviceInfo *d = nullptr;
+    rc = device_info(&d);
+    if (rc) return rc;
+    cudaError_t e = gqa::launch_pages_reserve(block_table, refcount, seqlens, n_new, k_pages, v_pages, B, G, M, page,
+                                              num_pages, c.row16, workspace, d->status,
+                                              reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail_cuda(e, "page reserve launch");
+    return GQA_OK;
+}
+
+int gqa_pages_fork(int32_t *block_table, int32_t *refcount, int32_t *seqlens, const int32_t *src, const int32_t *dst,
+                   int n, int B, int page, int num_pages, int M, gqa_stream_t stream) {
+    t_err[0] = 0;
+    int rc = check_pool(block_table, refcount, B, page, num_pages, M);
+    if (rc) return rc;
+    if (n <= 0) return fail(GQA_ERR_INVALID, "n must be positive");
+    if (n > 8192) return fail(GQA_ERR_UNSUPPORTED, "n=%d pairs above 8192", n);
+    if (!seqlens || !src || !dst) return fail(GQA_ERR_INVALID, "null tensor pointer");
+    if (misaligned(seqlens, 4) || misaligned(src, 4) || misaligned(dst, 4))
+        return fail(GQA_ERR_ALIGN, "seqlens, src and dst must be 4-byte aligned");
+    DeviceInfo *d = nullptr;
+    rc = device_info(&d);
+    if (rc) return rc;
+    cudaError_t e = gqa::launch_pages_fork(block_table, refcount, seqlens, src, dst, n, B, M, page, num_pages,
+                                           d->status, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail_cuda(e, "page fork launch");
+    return GQA_OK;
+}
+
+int gqa_pages_release(int32_t *block_table, int32_t *refcount, const int32_t *lengths, int B, int page, int num_pages,
+                      int M, gqa_stream_t stream) {
+    t_err[0] = 0;
+    int rc = check_pool(block_table, refcount, B, page, num_pages, M);
+    if (rc) return rc;
+    if (!lengths) return fail(GQA_ERR_INVALID, "null tensor pointer");
+    if (misaligned(lengths, 4)) return fail(GQA_ERR_ALIGN, "lengths must be 4-byte aligned");
+    DeviceInfo *d = nullptr;
+    rc = device_info(&d);
+    if (rc) return rc;
+    cudaError_t e = gqa::launch_pages_release(block_table, refcount, lengths, B, M, page, num_pages, d->status,
+                                              reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail_cuda(e, "page release launch");
+    return GQA_OK;
+}
+
 int gqa_selftest_wait_timeout(uint64_t limit_ns, int *waited, gqa_stream_t stream) {
     t_err[0] = 0;
     if (limit_ns == 0 || limit_ns > 10000000000ull)
@@ -596,6 +919,8 @@ int gqa_get_status(gqa_stream_t stream) {
     }
     if (word & 4u) return fail(GQA_ERR_INDEX, "an index check of the debug build failed (the access was skipped)");
     if (word & 2u) return fail(GQA_ERR_TIMEOUT, "a device-side wait ran out of time");
+    if (word & 8u)
+        return fail(GQA_ERR_PAGES, "a block table, reference count or page pool could not serve a call (skipped)");
     if (word & 1u) return fail(GQA_ERR_SEQLEN, "a seqlens entry was outside [0, T_cap] (clamped)");
     return GQA_OK;
 }

@@ -23,6 +23,7 @@ namespace gqa {
 enum : unsigned {
     STATUS_SEQLEN = 1u,   // a seqlens entry was outside [0, T_cap]
     STATUS_TIMEOUT = 2u,  // a bounded wait ran out
+    STATUS_PAGES = 8u,    // a block table, reference count or page pool could not serve a call
     STATUS_INDEX = 4u,    // an index check of the debug build failed (the access was skipped)
 };
 

@@ -102,4 +102,67 @@ cudaError_t launch_init_heads(const void *wk, const void *wv, void *ok, void *ov
                               long long n, int dtype, int mode, const float *weights, int select,
                               int num_sms, unsigned *status, cudaStream_t stream);
 
+// A K/V cache as the paged kernels see it: pools [num_pages, G, page, d_h] and a
+// block table [B, M], or (table null) a dense cache as one page per sequence.
+struct CacheView {
+    const int32_t *table;  // null: dense
+    int B, G, M;
+    int page;       // positions per page
+    int num_pages;  // pages of a pool (dense: B)
+    int cap;        // positions a sequence can hold (M * page; dense: T_cap)
+    int row16;      // 16-byte pieces of one row of d_h values
+};
+
+cudaError_t launch_cache_append(const void *k_new, const void *v_new, const int32_t *cu, const int32_t *seqlens,
+                                int32_t *seqlens_out, void *k_cache, void *v_cache, const CacheView &c, int N,
+                                int num_sms, unsigned *status, cudaStream_t stream);
+cudaError_t launch_cache_compact(void *k_cache, void *v_cache, const int32_t *seqlens, const int32_t *keep,
+                                 const int32_t *n_keep, int32_t *seqlens_out, const CacheView &c, int m,
+                                 unsigned *status, cudaStream_t stream);
+cudaError_t launch_pages_release(int32_t *table, int32_t *refcount, const int32_t *lengths, int B, int M, int page,
+                                 int P, unsigned *status, cudaStream_t stream);
+cudaError_t launch_pages_fork(int32_t *table, int32_t *refcount, int32_t *seqlens, const int32_t *src,
+                              const int32_t *dst, int n, int B, int M, int page, int P, unsigned *status,
+                              cudaStream_t stream);
+size_t pages_reserve_workspace(int B, int P);
+cudaError_t launch_pages_reserve(int32_t *table, int32_t *refcount, const int32_t *seqlens, const int32_t *n_new,
+                                 void *k_pages, void *v_pages, int B, int G, int M, int page, int P, int row16,
+                                 void *workspace, unsigned *status, cudaStream_t stream);
+
+// Causal attention over packed sequences (tcgen05).  tmq: [d_h, H, N] in boxes
+// of [64 dims x H/G heads x kPackRows / (H/G) positions]; tmk, tmv: [d_h, G, N]
+// in boxes of [64 x 1 x 128].
+struct PackedArgs {
+    const int32_t *cu;
+    void *out;
+    float scale;
+    int B, N, H, G, d_h;
+    unsigned *status;
+    uint64_t timeout_ns;
+    int window;
+};
+cudaError_t launch_prefill_packed(const PackedArgs &a, const CUtensorMap *tmq, const CUtensorMap *tmk,
+                                  const CUtensorMap *tmv, cudaStream_t stream);
+
+// Attention of a tree of drafted tokens over a dense or paged cache (tcgen05).
+// tmq as above over the B * n draft tokens; tmk, tmv: [d_h, page, G, num_pages]
+// in boxes of [64 x box x 1 x 1].
+struct TreeArgs {
+    const int32_t *seqlens;
+    const int64_t *mask;
+    const int32_t *n_draft;
+    void *out;
+    float scale;
+    int n, H, d_h;
+    int box;  // positions of one K/V load: divides 128, and the page unless that is one per sequence
+    CacheView cache;
+    void *workspace;
+    unsigned *status;
+    uint64_t timeout_ns;
+    int num_sms;
+};
+size_t decode_tree_workspace(int B, int n, int r, int d_h, int num_sms);
+cudaError_t launch_decode_tree(const TreeArgs &a, const CUtensorMap *tmq, const CUtensorMap *tmk,
+                               const CUtensorMap *tmv, cudaStream_t stream);
+
 }  // namespace gqa

@@ -1,0 +1,160 @@
+"""Causal prefill over packed prompts (gqa_prefill_packed) vs the 64-bit definition.
+
+The bound is derived in paged_reference.py; rows of no sequence keep what they held, bit for bit, and
+NaN around and between sequences reaches nobody.
+"""
+import pytest
+import torch
+
+import paged_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def inputs(cu, H, G, d, N=None, seed=0, std=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    N = N or max(1, cu[-1])
+    q, k, v = (torch.randn((N, h, d), generator=gen).mul_(std).to(torch.bfloat16) for h in (H, G, G))
+    return q, k, v
+
+
+def offsets(lens):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+def run(gqa, q, k, v, cu, **kw):
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    got = gqa.prefill_packed(q.cuda(), k.cuda(), v.cuda(), torch.tensor(cu, dtype=torch.int32).cuda(), out=out, **kw)
+    gqa.get_status()
+    assert got is out
+    return out.cpu()
+
+
+def compare(got, r, w, q):
+    inside = ~torch.isnan(r[:, 0, 0])
+    # rows of at most 128 keys carry P as two terms, but which tile a row is in is the kernel's
+    # affair: the one-term bound holds for all
+    ref.check(got[inside], r[inside], w[inside])
+    assert (got[~inside] == 7.0).all()
+
+
+@pytest.mark.parametrize("H,G,d", [(4, 4, 64), (4, 2, 128), (6, 2, 64), (8, 2, 128), (5, 1, 128), (7, 1, 64),
+                                   (16, 1, 128), (64, 1, 64), (65, 1, 64), (128, 1, 64)])
+@pytest.mark.parametrize("lens", [[1], [5, 1, 0, 130, 64], [300, 17], [0, 0, 129, 128, 127, 0]])
+def test_groups_and_lengths(gqa, H, G, d, lens):
+    cu = offsets(lens)
+    q, k, v = inputs(cu, H, G, d, seed=sum(lens) + H)
+    got = run(gqa, q, k, v, cu)
+    r, w = ref.prefill_packed(q, k, v, cu, d ** -0.5)
+    compare(got, r, w, q)
+
+
+@pytest.mark.parametrize("window", [1, 2, 31, 128, 200, 257, 1000])
+@pytest.mark.parametrize("H,G", [(2, 2), (6, 2), (8, 1)])
+def test_windows(gqa, window, H, G):
+    cu = offsets([3, 700, 129])
+    q, k, v = inputs(cu, H, G, 64, seed=window)
+    got = run(gqa, q, k, v, cu, window=window)
+    r, w = ref.prefill_packed(q, k, v, cu, 64 ** -0.5, window)
+    compare(got, r, w, q)
+
+
+def test_rows_outside_sequences_are_untouched_and_unread(gqa):
+    """cu_seqlens that starts late and ends early; the rows outside hold NaN."""
+    cu = [37, 167, 167, 300]
+    q, k, v = inputs(cu, 8, 2, 128, N=450, seed=3)
+    for x in (q, k, v):
+        x[:37] = float("nan")
+        x[300:] = float("nan")
+    got = run(gqa, q, k, v, cu)
+    r, w = ref.prefill_packed(q, k, v, cu, 128 ** -0.5)
+    compare(got, r, w, q)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_poisoned_sequence_poisons_no_other(gqa, value):
+    cu = offsets([70, 50, 200])
+    q, k, v = inputs(cu, 4, 1, 64, seed=4)
+    k[70:120] = value
+    v[70:120] = value
+    got = run(gqa, q, k, v, cu)
+    r, w = ref.prefill_packed(q, k, v, cu, 64 ** -0.5)
+    for a, z in ((0, 70), (120, 320)):
+        ref.check(got[a:z], r[a:z], w[a:z])
+
+
+def test_many_sequences_match_the_dense_call_and_themselves(gqa):
+    """200 prompts of 1 to 400 tokens; each against a call of its own, and twice the same bits."""
+    gen = torch.Generator().manual_seed(5)
+    lens = torch.randint(1, 401, (200,), generator=gen).tolist()
+    cu = offsets(lens)
+    q, k, v = inputs(cu, 8, 2, 64, seed=6)
+    got, again = run(gqa, q, k, v, cu), run(gqa, q, k, v, cu)
+    assert torch.equal(got, again)
+    r, w = ref.prefill_packed(q, k, v, cu, 64 ** -0.5)
+    compare(got, r, w, q)
+    for b in (0, 77, 199):
+        a, z = cu[b], cu[b + 1]
+        dense = gqa.prefill_causal(*(x[a:z][None].cuda() for x in (q, k, v)))[0].cpu()
+        ref.check(dense, r[a:z], w[a:z])
+
+
+def test_long_sequences_sampled(gqa):
+    """3000 + 5000 + 1 tokens: rows across all key tiles."""
+    cu = offsets([3001, 1, 5000])
+    q, k, v = inputs(cu, 8, 2, 128, seed=8)
+    got = run(gqa, q, k, v, cu)
+    for s in (0, 127, 128, 1500, 3000, 3001, 3002, 5555, 8001):
+        a = max(c for c in cu if c <= s)
+        for h in (0, 3, 7):
+            r, w = ref.attend(q[s:s + 1, h], k[a:s + 1, h // 4], v[a:s + 1, h // 4],
+                              torch.ones(1, s + 1 - a, dtype=torch.bool), 128 ** -0.5)
+            ref.check(got[s:s + 1, h], r, w)
+
+
+@pytest.mark.parametrize("scale", [1e-3, 0.5, 4.0])
+def test_scales_and_large_scores(gqa, scale):
+    """The running maximum moves by far more than the rescale threshold."""
+    cu = offsets([513])
+    q, k, v = inputs(cu, 2, 1, 64, seed=9)
+    k = (k.float() * torch.linspace(0.01, 1, 513)[:, None, None]).to(torch.bfloat16)
+    got = run(gqa, q, k, v, cu, scale=scale)
+    r, w = ref.prefill_packed(q, k, v, cu, scale)
+    # scores reach sum |q k| * scale ~ 64 * 0.64 * 4 * 1.44 < 2^8 in log2 units, 2^2 times what the
+    # bound's fp32 part assumes
+    d = (got.double() - r).abs()
+    assert (d <= ref.bound(r, w) + 4 * ref.FP32_PART * w).all()
+
+
+def test_bad_offsets_are_clamped_and_flagged(gqa):
+    q, k, v = inputs([0, 300], 4, 2, 64, seed=10)
+    for cu in ([0, 200, 100, 300], [-5, 300], [0, 301], [0, 1 << 30]):
+        out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        gqa.prefill_packed(q.cuda(), k.cuda(), v.cuda(), torch.tensor(cu, dtype=torch.int32).cuda(), out=out)
+        with pytest.raises(gqa.GQAError) as e:
+            gqa.get_status()
+        assert e.value.code == -7
+        gqa.get_status()
+
+
+def test_captured_replayed_and_on_another_stream(gqa):
+    cu = torch.tensor([0, 100, 333], dtype=torch.int32).cuda()
+    q, k, v = (x.cuda() for x in inputs([0, 333], 8, 2, 128, seed=11))
+    want = gqa.prefill_packed(q, k, v, cu)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = gqa.prefill_packed(q, k, v, cu, stream=side)
+    side.synchronize()
+    assert torch.equal(want, other)
+    out = torch.zeros_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gqa.prefill_packed(q, k, v, cu, out=out)
+    cu.copy_(torch.tensor([0, 200, 333], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, gqa.prefill_packed(q, k, v, cu))
+    gqa.get_status()

@@ -1,0 +1,122 @@
+"""Arguments that the packed, tree and paged calls refuse on the host (no GPU needed)."""
+import pytest
+import torch
+
+import kv_cache_decode_04_b200 as gqa
+
+L = gqa.lib
+A, BB, C, D, E, F, G_, H_ = (i << 32 for i in range(1, 9))  # addresses far apart
+
+
+def packed(**kw):
+    a = dict(q=A, k=BB, v=C, cu=D, out=E, B=2, N=100, H=8, G=2, d_h=64, scale=0.1, window=0, dt=gqa.GQA_BF16)
+    a.update(kw)
+    return L.gqa_prefill_packed(a["q"], a["k"], a["v"], a["cu"], a["out"], a["B"], a["N"], a["H"], a["G"], a["d_h"],
+                                a["scale"], a["window"], a["dt"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(G=3), -1), (dict(B=0), -1), (dict(N=0), -1), (dict(window=-1), -1), (dict(q=None), -1), (dict(cu=None), -1),
+    (dict(scale=0.0), -1), (dict(scale=float("inf")), -1), (dict(dt=gqa.GQA_F32), -2), (dict(d_h=96), -2),
+    (dict(H=258, G=2), -2), (dict(B=8193), -2), (dict(N=1 << 30), -2), (dict(k=BB + 8), -3), (dict(cu=D + 2), -3),
+    (dict(out=A), -1), (dict(out=BB + 16), -1)])
+def test_prefill_packed(kw, code):
+    assert packed(**kw) == code
+
+
+def tree(**kw):
+    a = dict(q=A, k=BB, v=C, table=D, sl=E, mask=F, nd=None, scale=0.1, out=G_, B=2, n=4, H=8, G=2, d_h=64, page=16,
+             P=10, M=5, dt=gqa.GQA_BF16, ws=H_, wsb=1 << 30)
+    a.update(kw)
+    return L.gqa_decode_tree(a["q"], a["k"], a["v"], a["table"], a["sl"], a["mask"], a["nd"], a["scale"], a["out"],
+                             a["B"], a["n"], a["H"], a["G"], a["d_h"], a["page"], a["P"], a["M"], a["dt"], a["ws"],
+                             a["wsb"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(G=3), -1), (dict(n=0), -1), (dict(n=65), -1), (dict(sl=None), -1), (dict(scale=-1.0), -1),
+    (dict(scale=float("nan")), -1), (dict(dt=gqa.GQA_F32), -2), (dict(dt=9), -2), (dict(d_h=32), -2),
+    (dict(H=258, G=2), -2), (dict(page=24), -2), (dict(page=0), -1), (dict(M=0), -1), (dict(M=1 << 28), -2),
+    (dict(table=None), -1), (dict(B=8193), -2), (dict(mask=F + 4), -3), (dict(out=A), -1), (dict(q=A + 2), -3),
+    (dict(M=1 << 26, B=8000), -2)])
+def test_decode_tree(kw, code):
+    assert tree(**kw) == code
+    assert gqa.lib.gqa_last_error_string()
+
+
+def append(**kw):
+    a = dict(kn=A, vn=BB, cu=C, sl=D, slo=E, k=F, v=G_, table=None, B=2, N=8, G=2, d_h=64, page=100, P=2, M=1,
+             dt=gqa.GQA_F32)
+    a.update(kw)
+    return L.gqa_cache_append(a["kn"], a["vn"], a["cu"], a["sl"], a["slo"], a["k"], a["v"], a["table"], a["B"], a["N"],
+                              a["G"], a["d_h"], a["page"], a["P"], a["M"], a["dt"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(N=0), -1), (dict(B=0), -1), (dict(kn=None), -1), (dict(P=3), -1), (dict(slo=D + 4), -1), (dict(v=F), -1),
+    (dict(kn=F), -1), (dict(dt=5), -2), (dict(d_h=80), -2), (dict(kn=A + 4), -3), (dict(sl=D + 1), -3)])
+def test_cache_append(kw, code):
+    assert append(**kw) == code
+
+
+def compact(**kw):
+    a = dict(k=A, v=BB, table=C, sl=D, keep=E, nk=F, slo=G_, B=2, m=4, G=2, d_h=64, page=16, P=9, M=3,
+             dt=gqa.GQA_BF16)
+    a.update(kw)
+    return L.gqa_cache_compact(a["k"], a["v"], a["table"], a["sl"], a["keep"], a["nk"], a["slo"], a["B"], a["m"],
+                               a["G"], a["d_h"], a["page"], a["P"], a["M"], a["dt"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(m=0), -1), (dict(m=65), -1), (dict(keep=None), -1), (dict(slo=D), -1), (dict(slo=E), -1), (dict(v=A), -1),
+    (dict(d_h=256), -2), (dict(k=A + 8), -3), (dict(nk=F + 2), -3)])
+def test_cache_compact(kw, code):
+    assert compact(**kw) == code
+
+
+def test_pages():
+    def reserve(**kw):
+        a = dict(t=A, r=BB, sl=C, n=D, k=E, v=F, B=2, G=2, d_h=64, page=16, P=10, M=5, dt=gqa.GQA_BF16, ws=G_,
+                 wsb=1 << 20)
+        a.update(kw)
+        return L.gqa_pages_reserve(a["t"], a["r"], a["sl"], a["n"], a["k"], a["v"], a["B"], a["G"], a["d_h"],
+                                   a["page"], a["P"], a["M"], a["dt"], a["ws"], a["wsb"], None)
+
+    for kw, code in [(dict(t=None), -1), (dict(r=A), -1), (dict(P=0), -1), (dict(v=E), -1), (dict(dt=3), -2),
+                     (dict(ws=None), -5), (dict(wsb=10), -5), (dict(ws=G_ + 16), -3), (dict(n=None), -1)]:
+        assert reserve(**kw) == code, kw
+    assert L.gqa_pages_fork(A, BB, C, D, E, 0, 4, 16, 10, 5, None) == -1
+    assert L.gqa_pages_fork(A, BB, C, D, E, 8193, 4, 16, 10, 5, None) == -2
+    assert L.gqa_pages_fork(A, BB, C, None, E, 2, 4, 16, 10, 5, None) == -1
+    assert L.gqa_pages_fork(A, BB, C + 1, D, E, 2, 4, 16, 10, 5, None) == -3
+    assert L.gqa_pages_release(A, BB, None, 4, 16, 10, 5, None) == -1
+    assert L.gqa_pages_release(A, BB, C, 4, 0, 10, 5, None) == -1
+    assert L.gqa_pages_release(A, BB, C, 4, 1 << 28, 10, 64, None) == -2
+
+
+def test_the_binding_checks_shapes_types_and_devices():
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)  # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(ValueError):
+        gqa.prefill_packed(z(8, 4, 64), z(9, 2, 64), z(9, 2, 64), i(2))
+    with pytest.raises(ValueError):
+        gqa.prefill_packed(z(8, 4, 64), z(8, 2, 64), z(8, 2, 64), torch.zeros(2, dtype=torch.int64))
+    with pytest.raises(TypeError):
+        gqa.prefill_packed(z(8, 4, 64), z(8, 2, 64), z(8, 2, 64, dt=torch.float32), i(2))
+    with pytest.raises(TypeError):  # not a CUDA tensor
+        gqa.prefill_packed(z(8, 4, 64), z(8, 2, 64), z(8, 2, 64), i(2))
+    with pytest.raises(ValueError):  # tree_mask of another type
+        gqa.decode_tree(z(2, 3, 4, 64), z(2, 2, 9, 64), z(2, 2, 9, 64), i(2), tree_mask=i(2, 3))
+    with pytest.raises(ValueError):  # a dense cache of another batch
+        gqa.decode_tree(z(2, 3, 4, 64), z(5, 2, 9, 64), z(5, 2, 9, 64), i(2))
+    with pytest.raises(ValueError):
+        gqa.decode_tree(z(2, 3, 4, 64), z(5, 2, 16, 64), z(5, 2, 16, 64), i(2), block_table=i(3, 4))
+    with pytest.raises(TypeError):
+        gqa.cache_append(z(4, 2, 64), z(4, 2, 64), i(3), i(2), z(2, 2, 9, 64, dt=torch.float32),
+                         z(2, 2, 9, 64, dt=torch.float32))
+    with pytest.raises(ValueError):
+        gqa.cache_compact(z(2, 2, 9, 64), z(2, 2, 9, 64), i(2), i(3, 4))
+    with pytest.raises(ValueError):
+        gqa.pages_reserve(i(2, 4), i(6), i(2), i(2), z(5, 2, 16, 64), z(5, 2, 16, 64))
+    with pytest.raises(ValueError):
+        gqa.pages_fork(i(2, 4), i(6), i(2), i(2), i(1), page_size=16)
