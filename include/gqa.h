@@ -387,7 +387,7 @@ GQA_API int gqa_prefill_packed(const void *q, const void *k, const void *v, cons
  * is zero.  Positions past T_b + n_draft[b] are never used, whatever they hold.
  * A missing page counts as zeros and flags GQA_ERR_PAGES; lengths and counts out
  * of range are clamped and flag GQA_ERR_SEQLEN.
- * Supported: bf16, d_h 64 or 128, 1 <= n <= 64, H/G <= 128, B <= 8192, page a
+ * Supported: bf16, d_h 64 or 128, 1 <= n <= 64, H/G <= 128, B <= 8000, page a
  * multiple of 16 (dense: any T_cap); scale finite and positive.
  */
 GQA_API size_t gqa_decode_tree_workspace_bytes(int B, int n, int H, int G, int d_h);

@@ -21,6 +21,7 @@ Calls (same names as the C ABI, without the ``gqa_`` prefix):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -386,17 +387,38 @@ def layer_decode_step(h, W_Q, W_K, W_V, W_O, k_cache, v_cache, seqlens, scale=No
 # ---------------------------------------------------------------- packed prompts, paged caches
 
 
-def _same(what, device, *named):
-    """Every tensor is a contiguous CUDA tensor on `device`, the current one."""
-    for name, t in named:
-        if t.device != device:
-            raise ValueError("%s is on %s, %s on %s" % (name, t.device, what, device))
+# These calls are short on the GPU, so what they spend here counts: tensors are checked in one
+# pass, and the current stream is asked for by its handle (0.1 us; torch.cuda.current_stream()
+# builds an object around it in 3 us).
+
+
+def _ready(names, *tensors):
+    """Every tensor (None: absent) is contiguous and on the current CUDA device, whose index it returns."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            break
+    else:
+        if index >= 0 and torch._C._cuda_getDevice() == index:
+            return index
+    for name, t in zip(names.split(), tensors):
+        if t is None:
+            continue
+        if t.get_device() < 0:
+            raise TypeError("%s must be a CUDA tensor" % name)
+        if t.get_device() != index:
+            raise ValueError("%s is on %s, not on cuda:%d" % (name, t.device, index))
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
-    if device.type != "cuda":
-        raise TypeError("%s must be a CUDA tensor" % what)
-    if device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, which is not the current device" % (what, device))
+    raise ValueError("the tensors are on cuda:%d, which is not the current device" % index)
+
+
+def _handle(stream, index):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _int32(name, t, *shape):
@@ -404,13 +426,14 @@ def _int32(name, t, *shape):
         raise ValueError("%s must be int32 %s" % (name, list(shape)))
 
 
-def _empty(stream, *size, dtype, device):
-    """torch.empty whose memory belongs to `stream` (None: the current stream), so that the
-    allocator does not hand it on while a kernel queued there still uses it."""
-    if stream is None:
-        return torch.empty(size, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(size, dtype=dtype, device=device)
+def _empty(stream, like, size=None, dtype=None):
+    """An uninitialised tensor like `like` (or of another size and dtype) whose memory belongs to `stream`
+    (None: the current stream), so that the allocator does not hand it on while a kernel queued there
+    still uses it."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _empty(None, like, size, dtype)
+    return torch.empty_like(like) if size is None else like.new_empty(size, dtype=dtype)
 
 
 def _cache(k_cache, v_cache, block_table, B):
@@ -425,10 +448,6 @@ def _cache(k_cache, v_cache, block_table, B):
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be int32 [B, M] with B = %d" % B)
     return block_table.data_ptr(), G, page, P, block_table.shape[1]
-
-
-def _tensors(**named):
-    return [(n, t) for n, t in named.items() if t is not None]
 
 
 def prefill_packed(q, k, v, cu_seqlens, scale=None, out=None, stream=None, window=0):
@@ -448,13 +467,13 @@ def prefill_packed(q, k, v, cu_seqlens, scale=None, out=None, stream=None, windo
     B = cu_seqlens.numel() - 1
     _int32("cu_seqlens", cu_seqlens, B + 1)
     if out is None:
-        out = _empty(stream, N, H, d_h, dtype=q.dtype, device=q.device)
+        out = _empty(stream, q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
-    _same("q", q.device, ("q", q), ("k", k), ("v", v), ("cu_seqlens", cu_seqlens), ("out", out))
+    index = _ready("q k v cu_seqlens out", q, k, v, cu_seqlens, out)
     _check(lib.gqa_prefill_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), out.data_ptr(), B,
-                                  N, H, G, d_h, 1.0 / math.sqrt(d_h) if scale is None else float(scale), int(window),
-                                  code, _stream(stream)))
+                                  N, H, G, d_h, 1.0 / math.sqrt(d_h) if scale is None else scale, window, code,
+                                  _handle(stream, index)))
     return out
 
 
@@ -463,6 +482,11 @@ def decode_tree_workspace_bytes(B, n, H, G, d_h) -> int:
     if size == 0:
         raise GQAError(-1, "invalid draft shape or device: " + lib.gqa_last_error_string().decode())
     return size
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(index, B, n, H, G, d_h):
+    return decode_tree_workspace_bytes(B, n, H, G, d_h)
 
 
 def decode_tree(q, k_cache, v_cache, seqlens, tree_mask=None, n_draft=None, block_table=None, scale=None, out=None,
@@ -488,19 +512,20 @@ def decode_tree(q, k_cache, v_cache, seqlens, tree_mask=None, n_draft=None, bloc
     if n_draft is not None:
         _int32("n_draft", n_draft, B)
     if out is None:
-        out = _empty(stream, B, n, H, d_h, dtype=q.dtype, device=q.device)
+        out = _empty(stream, q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
+    index = _ready("q k_cache v_cache seqlens tree_mask n_draft block_table out workspace", q, k_cache, v_cache,
+                   seqlens, tree_mask, n_draft, block_table, out, workspace)
     if workspace is None:
-        workspace = _empty(stream, decode_tree_workspace_bytes(B, n, H, G, d_h), dtype=torch.uint8, device=q.device)
-    _same("q", q.device, *_tensors(q=q, k_cache=k_cache, v_cache=v_cache, seqlens=seqlens, tree_mask=tree_mask,
-                                   n_draft=n_draft, block_table=block_table, out=out, workspace=workspace))
+        size = _tree_workspace(index, B, n, H, G, d_h)
+        workspace = _empty(stream, q, size, torch.uint8)
+    else:
+        size = workspace.numel() * workspace.element_size()
     _check(lib.gqa_decode_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, seqlens.data_ptr(),
-                               None if tree_mask is None else tree_mask.data_ptr(),
-                               None if n_draft is None else n_draft.data_ptr(),
-                               1.0 / math.sqrt(d_h) if scale is None else float(scale), out.data_ptr(), B, n, H, G,
-                               d_h, page, P, M, code, workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), _stream(stream)))
+                               _ptr(tree_mask), _ptr(n_draft), 1.0 / math.sqrt(d_h) if scale is None else scale,
+                               out.data_ptr(), B, n, H, G, d_h, page, P, M, code, workspace.data_ptr(), size,
+                               _handle(stream, index)))
     return out
 
 
@@ -522,15 +547,14 @@ def cache_append(k_new, v_new, cu_seqlens, seqlens, k_cache, v_cache, block_tabl
     _int32("seqlens", seqlens, B)
     _int32("cu_seqlens", cu_seqlens, B + 1)
     if seqlens_out is None:
-        seqlens_out = _empty(stream, B, dtype=torch.int32, device=k_cache.device)
+        seqlens_out = _empty(stream, seqlens)
     else:
         _int32("seqlens_out", seqlens_out, B)
-    _same("k_cache", k_cache.device, *_tensors(k_cache=k_cache, v_cache=v_cache, k_new=k_new, v_new=v_new,
-                                               cu_seqlens=cu_seqlens, seqlens=seqlens, seqlens_out=seqlens_out,
-                                               block_table=block_table))
+    index = _ready("k_cache v_cache k_new v_new cu_seqlens seqlens seqlens_out block_table", k_cache, v_cache, k_new,
+                   v_new, cu_seqlens, seqlens, seqlens_out, block_table)
     _check(lib.gqa_cache_append(k_new.data_ptr(), v_new.data_ptr(), cu_seqlens.data_ptr(), seqlens.data_ptr(),
                                 seqlens_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, B, N, G, d_h,
-                                page, P, M, code, _stream(stream)))
+                                page, P, M, code, _handle(stream, index)))
     return seqlens_out
 
 
@@ -549,14 +573,14 @@ def cache_compact(k_cache, v_cache, seqlens, keep, n_keep=None, block_table=None
     if n_keep is not None:
         _int32("n_keep", n_keep, B)
     if seqlens_out is None:
-        seqlens_out = _empty(stream, B, dtype=torch.int32, device=k_cache.device)
+        seqlens_out = _empty(stream, seqlens)
     else:
         _int32("seqlens_out", seqlens_out, B)
-    _same("k_cache", k_cache.device, *_tensors(k_cache=k_cache, v_cache=v_cache, seqlens=seqlens, keep=keep,
-                                               n_keep=n_keep, seqlens_out=seqlens_out, block_table=block_table))
+    index = _ready("k_cache v_cache seqlens keep n_keep seqlens_out block_table", k_cache, v_cache, seqlens, keep,
+                   n_keep, seqlens_out, block_table)
     _check(lib.gqa_cache_compact(k_cache.data_ptr(), v_cache.data_ptr(), table, seqlens.data_ptr(), keep.data_ptr(),
-                                 None if n_keep is None else n_keep.data_ptr(), seqlens_out.data_ptr(), B, m, G,
-                                 k_cache.shape[3], page, P, M, code, _stream(stream)))
+                                 _ptr(n_keep), seqlens_out.data_ptr(), B, m, G, k_cache.shape[3], page, P, M, code,
+                                 _handle(stream, index)))
     return seqlens_out
 
 
@@ -566,6 +590,11 @@ def _pool(block_table, refcount):
     if refcount.dtype != torch.int32 or refcount.dim() != 1:
         raise ValueError("refcount must be int32 [P]")
     return block_table.shape[0], block_table.shape[1], refcount.shape[0]
+
+
+@functools.lru_cache(maxsize=256)
+def _reserve_workspace(B, P):
+    return int(lib.gqa_pages_reserve_workspace_bytes(B, P))
 
 
 def pages_reserve(block_table, refcount, seqlens, n_new, k_pages, v_pages, workspace=None, stream=None):
@@ -579,14 +608,16 @@ def pages_reserve(block_table, refcount, seqlens, n_new, k_pages, v_pages, works
     code = _dtype_code(k_pages)
     _int32("seqlens", seqlens, B)
     _int32("n_new", n_new, B)
+    index = _ready("k_pages v_pages block_table refcount seqlens n_new workspace", k_pages, v_pages, block_table,
+                   refcount, seqlens, n_new, workspace)
     if workspace is None:
-        workspace = _empty(stream, int(lib.gqa_pages_reserve_workspace_bytes(B, P)), dtype=torch.uint8,
-                           device=k_pages.device)
-    _same("k_pages", k_pages.device, *_tensors(k_pages=k_pages, v_pages=v_pages, block_table=block_table,
-                                               refcount=refcount, seqlens=seqlens, n_new=n_new, workspace=workspace))
+        size = _reserve_workspace(B, P)
+        workspace = _empty(stream, k_pages, size, torch.uint8)
+    else:
+        size = workspace.numel() * workspace.element_size()
     _check(lib.gqa_pages_reserve(block_table.data_ptr(), refcount.data_ptr(), seqlens.data_ptr(), n_new.data_ptr(),
                                  k_pages.data_ptr(), v_pages.data_ptr(), B, G, k_pages.shape[3], page, P, M, code,
-                                 workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+                                 workspace.data_ptr(), size, _handle(stream, index)))
 
 
 def pages_fork(block_table, refcount, seqlens, src, dst, page_size, stream=None):
@@ -597,20 +628,18 @@ def pages_fork(block_table, refcount, seqlens, src, dst, page_size, stream=None)
     n = src.numel()
     _int32("src", src, n)
     _int32("dst", dst, n)
-    _same("block_table", block_table.device, ("block_table", block_table), ("refcount", refcount),
-          ("seqlens", seqlens), ("src", src), ("dst", dst))
+    index = _ready("block_table refcount seqlens src dst", block_table, refcount, seqlens, src, dst)
     _check(lib.gqa_pages_fork(block_table.data_ptr(), refcount.data_ptr(), seqlens.data_ptr(), src.data_ptr(),
-                              dst.data_ptr(), n, B, int(page_size), P, M, _stream(stream)))
+                              dst.data_ptr(), n, B, page_size, P, M, _handle(stream, index)))
 
 
 def pages_release(block_table, refcount, lengths, page_size, stream=None):
     """Gives back the pages that lengths[b] positions of each sequence do not need (0: all of them)."""
     B, M, P = _pool(block_table, refcount)
     _int32("lengths", lengths, B)
-    _same("block_table", block_table.device, ("block_table", block_table), ("refcount", refcount),
-          ("lengths", lengths))
-    _check(lib.gqa_pages_release(block_table.data_ptr(), refcount.data_ptr(), lengths.data_ptr(), B, int(page_size),
-                                 P, M, _stream(stream)))
+    index = _ready("block_table refcount lengths", block_table, refcount, lengths)
+    _check(lib.gqa_pages_release(block_table.data_ptr(), refcount.data_ptr(), lengths.data_ptr(), B, page_size, P, M,
+                                 _handle(stream, index)))
 
 
 def get_status(stream=None):

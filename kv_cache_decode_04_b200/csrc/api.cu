@@ -628,6 +628,7 @@ int gqa_prefill_packed(const void *q, const void *k, const void *v, const int32_
     a.status = d->status;
     a.timeout_ns = wait_timeout_ns();
     a.window = window;
+    a.num_sms = d->num_sms;
     cudaError_t e = gqa::launch_prefill_packed(a, &tmq, &tmk, &tmv, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail_cuda(e, "packed prefill launch");
     return GQA_OK;
@@ -669,7 +670,7 @@ size_t gqa_decode_tree_workspace_bytes(int B, int n, int H, int G, int d_h) {
     }
     DeviceInfo *d = nullptr;
     if (device_info(&d)) return 0;
-    return gqa::decode_tree_workspace(B, n, H / G, d_h, d->num_sms);
+    return gqa::decode_tree_workspace(n, H / G, d_h, d->num_sms);
 }
 
 int gqa_decode_tree(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
@@ -690,8 +691,9 @@ int gqa_decode_tree(const void *q, const void *k_cache, const void *v_cache, con
     rc = cache_view(&c, block_table, B, G, d_h, page, num_pages, M, dt);
     if (rc) return rc;
     if (block_table && page % 16) return fail(GQA_ERR_UNSUPPORTED, "page=%d must be a multiple of 16", page);
+    if (B > 8000) return fail(GQA_ERR_UNSUPPORTED, "tree decode needs B <= 8000 (got %d)", B);
     const long long pt = 128 / r, blocks = (n + pt - 1) / pt;
-    if ((long long)B * G * blocks * ((c.cap + 127ll) / 128) >= (1ll << 31) || (long long)B * n * H >= (1ll << 31))
+    if ((long long)B * G * blocks * ((c.cap + 127ll) / 128 + 2) >= (1ll << 31) || (long long)B * n * H >= (1ll << 31))
         return fail(GQA_ERR_UNSUPPORTED, "too many key tiles or query rows for one call");
     if (misaligned(q, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(out, 16) ||
         misaligned(seqlens, 4) || misaligned(tree_mask, 8) || misaligned(n_draft, 4))
@@ -702,7 +704,7 @@ int gqa_decode_tree(const void *q, const void *k_cache, const void *v_cache, con
     DeviceInfo *d = nullptr;
     rc = device_info(&d);
     if (rc) return rc;
-    const size_t need = gqa::decode_tree_workspace(B, n, r, d_h, d->num_sms);
+    const size_t need = gqa::decode_tree_workspace(n, r, d_h, d->num_sms);
     if (!workspace || workspace_bytes < need)
         return fail(GQA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                     workspace ? workspace_bytes : (size_t)0);

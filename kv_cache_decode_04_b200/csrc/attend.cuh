@@ -1,12 +1,38 @@
-// attend.cuh -- what the packed prefill and the draft-tree decode share: rows
-// of (token, query head) packed into M = 128 tensor-core tiles, and the online
-// softmax of one [128 x 128] score tile held in tensor memory.
+// attend.cuh -- the attention pipeline that the packed prefill and the
+// draft-tree decode share (sm_100a): rows of (token, query head) packed into
+// M = 128 tensor-core tiles, pieces of key tiles streamed through shared
+// memory, online softmax in tensor memory, persistent CTAs.
 //
 // Row packing.  The r = H/G query heads of a group read the same K/V head, so
 // the rows of one tile are the (token, head) pairs of PT = floor(128 / r)
 // consecutive tokens: row = token * r + head.  One TMA box of [64 dims x r
 // heads x PT tokens] lays them out in that order.  A few tokens then fill a
 // tile as well as many do, whatever r is.
+//
+// A piece is one or two row tiles against a run of consecutive 128-key tiles.
+// A CTA works through pieces that a policy hands to every role in the same
+// order, and nothing waits for a piece to end but the row tile's own threads:
+// the next piece's Q, K and V are loaded, and its first scores computed, while
+// the last one's output is written.
+//   PAIR = 1: two row tiles (the two softmax warpgroups, one each) share every
+//     key tile.
+//   PAIR = 0: one row tile; the warpgroups take alternate key tiles, each with
+//     its own maximum, sum and O, merged at the end of the piece.
+//
+// Roles (384 threads):
+//   warps 0-3, 4-7  softmax and epilogue of row tile / key parity 0, 1: one
+//                   thread per row = tensor-memory lane
+//   warp 8          K tiles and Q rows by TMA     warp 11  V tiles by TMA
+//   warp 9          allocates tensor memory; one lane issues every tcgen05.mma
+//   warp 10         the policy's (the packed prefill's work list)
+// Tensor memory: S0/P0, S1/P1 (128 columns each), O0, O1 (128 each).  P (bf16)
+// overwrites its S block; the S of a later tile is issued behind the P.V that
+// reads that P, and MMAs of one thread complete in order.
+//
+// What bounds it: one key tile of two row tiles is 2,048 cycles of tensor time
+// and takes about 3,600, the period of one row tile's chain S -> softmax -> P
+// -> P.V (as in prefill.cu).  With one row tile the two parities overlap and a
+// tile takes the 2,430 cycles that HBM needs for its 64 KB.
 #pragma once
 
 #include "common.cuh"
@@ -28,7 +54,27 @@ constexpr int kLaunchRegs = 168;
 constexpr int kLowRegs = 136;
 constexpr int kHighRegs = 184;
 static_assert(2 * 128 * kHighRegs + 128 * kLowRegs <= kThreads * kLaunchRegs, "register split");
-constexpr uint32_t kTmemCols = 512;  // S0/P0, S1/P1 (128 columns each), O0, O1 (128 each)
+constexpr uint32_t kTmemCols = 512;
+
+// Shared memory of the pipeline: NQ buffers of PAIR + 1 Q tiles, ST-stage K
+// and V rings, barriers, the (m, l) exchange.  192 KB or less of tiles leaves
+// room for the policies' lists.
+template <int D, int PAIR>
+struct Layout {
+    static constexpr int HALVES = D / 64;
+    static constexpr int TILE = HALVES * kHalf;  // [128 x D] bf16
+    // two Q buffers wherever they fit beside the rings: the next piece's rows then
+    // never wait for the last scores of this one
+    static constexpr int NQ = (D == 128 && PAIR) ? 1 : 2;
+    static constexpr int ST = D == 128 ? 2 : 4;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = NQ * (PAIR + 1) * TILE;
+    static constexpr int OFF_V = OFF_K + ST * TILE;
+    static constexpr int OFF_BAR = OFF_V + ST * TILE;
+    static constexpr int OFF_ML = OFF_BAR + 384;              // [2][128] (m, l) of the two parities
+    static constexpr int OFF_POLICY = OFF_ML + (PAIR ? 0 : 2 * 128 * 8);  // what the policy keeps
+    static constexpr int SMEM = 1024 + OFF_POLICY;
+};
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, uint64_t *bar, int x, int y,
                                             int z, int w, uint64_t policy) {
@@ -66,28 +112,36 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64
 }
 
 // One online-softmax step for this thread's query row (its tensor-memory lane):
-// reads the 128 scores at tS, lets `mask(sr)` set hidden ones to -inf, moves
-// the running maximum m (log2 units) and the sum l, and writes P = 2^(s - m)
-// as bf16 pairs over the first 64 columns at tS.
+// reads the scores at tS, moves the running maximum m (log2 units) and the sum
+// l, and writes P = 2^(s - m) as bf16 pairs over the first 64 columns at tS.
 //   - The maximum moves (and O at tO is rescaled) only when it grows by more
 //     than 8, so p <= 2^8: numerator and denominator use the same stale one.
 //   - `first`: O holds nothing of this row yet.  Otherwise the P.V that last
 //     wrote O is complete, because the S just read was issued behind it.
-//   - split_p: P is carried as P_hi + P_lo, two bf16 terms (about 16
-//     significant bits), P_lo in columns 64..127.  For rows that see so few
-//     keys that the rounding of P does not average out.
 //   - m = -inf (no key seen yet): every score is -inf and p = 0.
+//   - PLAIN: a whole tile that every row sees.  Otherwise only the first 32 *
+//     nch columns are read and written, `mask(sr)` sets hidden scores to -inf,
+//     and with `split_p` P is carried as P_hi + P_lo, two bf16 terms (about 16
+//     significant bits), P_lo in columns 64..127: for rows that see so few keys
+//     that the rounding of P does not average out.
 // The row sum adds the unrounded p in fp32.
-template <int D, typename Mask>
+template <int D, bool PLAIN, typename Mask>
 __device__ __forceinline__ void softmax_step(uint32_t tS, uint32_t tO, float scale_log2, bool first, bool split_p,
-                                             float &m, float &l, Mask mask) {
+                                             int nch, float &m, float &l, Mask mask) {
     uint32_t sr[4][32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tc::ld32(tS + c * 32, sr[c]);
+    for (int c = 0; c < 4; ++c) {
+        if (PLAIN || c < nch) {
+            tc::ld32(tS + c * 32, sr[c]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) sr[c][e] = __float_as_uint(-INFINITY);
+        }
+    }
     tc::wait_ld();
 #pragma unroll
     for (int c = 0; c < 4; ++c) tc::hold32(sr[c]);
-    mask(sr);
+    if constexpr (!PLAIN) mask(sr);
     // row maximum of the raw scores (the scale is positive), eight partial maxima
     float mx8[8];
 #pragma unroll
@@ -115,9 +169,10 @@ __device__ __forceinline__ void softmax_step(uint32_t tS, uint32_t tO, float sca
     const float mu = m == -INFINITY ? 0.f : m;
     const uint64_t sc2 = f32x2_pack(scale_log2, scale_log2), nm2 = f32x2_pack(-mu, -mu);
     uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
-    if (!split_p) {
+    if (PLAIN || !split_p) {
 #pragma unroll
         for (int c4 = 0; c4 < 4; ++c4) {
+            if (!PLAIN && c4 >= nch) continue;
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -132,8 +187,11 @@ __device__ __forceinline__ void softmax_step(uint32_t tS, uint32_t tO, float sca
             tc::st16(tS + c4 * 16, pk);
         }
     } else {
+        // P_lo of chunk c4 goes to columns 64 + 16 c4, which chunks 2 and 3 of S
+        // occupied: their scores are in registers by now
 #pragma unroll
         for (int c4 = 0; c4 < 4; ++c4) {
+            if (c4 >= nch) continue;
 #pragma unroll
             for (int e4 = 0; e4 < 4; ++e4) {
                 uint32_t ph[4], pl[4];
@@ -174,21 +232,513 @@ __device__ __forceinline__ void softmax_step(uint32_t tS, uint32_t tO, float sca
     tc::wait_st();
 }
 
-// Zeroes rows [r0, 128) of a [128 x D] V tile (D / 64 swizzled boxes): P is 0
-// there, but 0 times what lies past a sequence's end must stay 0.  One warp;
-// the fence makes the writes visible to the tensor core's reads.
-template <int D>
-__device__ __forceinline__ void zero_tail_rows(uint8_t *tile, int r0, int lane) {
-    const int n = (kKeys - r0) * (D / 64) * 8;  // 16-byte pieces
-    for (int i = lane; i < n; i += 32) {
-        const int row = r0 + i / ((D / 64) * 8), rem = i % ((D / 64) * 8);
-        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
-                         smem_u32(tile + (rem >> 3) * kHalf + row * 128 + (rem & 7) * 16)),
-                     "r"(0u)
-                     : "memory");
+// Writes 8 NP values of each lane's row (bf16 pairs in w, NP pieces of 16
+// bytes) to out + row * D + col; row < 0: nothing.  NP lanes first exchange
+// their pieces (a transpose by shuffles), so that each store instruction
+// covers 16 NP consecutive bytes of a row: one thread storing its own row
+// touches 32 lines per instruction, and those stores took 2.2 us of a
+// [2 x 128 x 128] epilogue.
+template <int D, int NP>
+__device__ __forceinline__ void store_rows(__nv_bfloat16 *out, int row, int col, uint32_t (&w)[4 * NP]) {
+    const int lane = threadIdx.x & 31, a = lane & (NP - 1);
+#pragma unroll
+    for (int s = 1; s < NP; s <<= 1) {
+        const bool up = (lane & s) != 0;
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            if (k & s) continue;
+            // pieces k and k | s: this lane keeps the one on its side and gives the other
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t &lo = w[4 * k + i], &hi = w[4 * (k | s) + i];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
+                if (up) lo = got; else hi = got;
+            }
+        }
     }
-    fence_proxy_async_smem();
-    __syncwarp();
+    // piece k now is piece a of the row of lane (lane & ~(NP - 1)) + k
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const int rk = __shfl_sync(0xffffffffu, row, (lane & ~(NP - 1)) + k);
+        if (rk >= 0)
+            *reinterpret_cast<uint4 *>(out + (size_t)rk * D + col + a * 8) =
+                make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+}
+
+// What the pipeline needs to know of a piece; policies add their own.
+struct PieceBase {
+    // keys of row tile 0 and 1, from the first key of the piece's first tile on (0:
+    // the tile has no rows).  Row tile i visits ceil(k_i / 128) tiles.
+    int k0, k1;
+    int v_end;   // keys from there on that belong to the sequence: V rows past them are cleared
+    bool split;  // carry P as two bf16 terms
+    __device__ int tiles() const { return (max(k0, k1) + kKeys - 1) / kKeys; }
+};
+
+__device__ __forceinline__ int chunks_of(int keys, int j) {  // 32-key chunks of tile j that hold keys
+    return min(4, (keys - j * kKeys + 31) / 32);
+}
+
+template <int D, int PAIR>
+struct Barriers {
+    static constexpr int ST = Layout<D, PAIR>::ST;
+    uint64_t *q_full, *q_empty;                          // [2] (NQ used)
+    uint64_t *k_full, *k_empty, *v_full, *v_empty;       // [ST]
+    uint64_t *s_full, *p_ready;                          // [2] per softmax warpgroup
+    // [2] a piece's last P.V is complete.  One per softmax warpgroup, committed only for
+    // pieces in which it has rows: no later phase can complete before it has seen this one.
+    uint64_t *o_done;
+    uint64_t *meet;                                      // the two warpgroups (PAIR = 0)
+    uint64_t *drain;
+    uint64_t *policy;                                    // [16]
+    uint32_t *tmem_slot;
+    int *abort_flag;
+    __device__ explicit Barriers(uint8_t *sm) {
+        uint64_t *b = reinterpret_cast<uint64_t *>(sm + Layout<D, PAIR>::OFF_BAR);
+        q_full = b;
+        q_empty = b + 2;
+        s_full = b + 4;
+        p_ready = b + 6;
+        o_done = b + 8;
+        meet = b + 10;
+        drain = b + 11;
+        k_full = b + 12;
+        k_empty = k_full + ST;
+        v_full = k_empty + ST;
+        v_empty = v_full + ST;
+        policy = b + 28;
+        tmem_slot = reinterpret_cast<uint32_t *>(b + 44);
+        abort_flag = reinterpret_cast<int *>(b + 45);
+    }
+    __device__ void init() const {  // one thread
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&q_full[s], 1);
+            mbar_init(&q_empty[s], 1);
+            mbar_init(&s_full[s], 1);
+            mbar_init(&p_ready[s], 128);
+            mbar_init(&o_done[s], 1);
+        }
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], 1);
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], 1);
+        }
+        mbar_init(meet, 256);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+    }
+};
+
+// Everything after set-up: all threads of the CTA, tensor memory allocated at
+// `tmem`.  Pol is the policy:
+//   Pol::Piece                    a PieceBase with more
+//   Pol::Iter(pol, whole_warp)    walks the CTA's pieces: bool next(Piece &), the same for all lanes
+//                                 when a whole warp calls it, and done() when the calling role is
+//                                 through with a piece (one call per piece)
+//   pol.kv(piece, tile, K or V, stage address, barrier, lane)  loads of a tile, by a whole warp
+//   pol.kv_look(piece, tile, lane)  what kv() needs from memory, asked for before the stage is free
+//   pol.q(piece, row tile, address, barrier)  loads of Q rows, by one lane; pol.q_bytes() each
+//   pol.row(piece, row tile, row)  -> Pol::Row, the thread's row;  pol.masked(piece, row, tile)
+//   pol.mask(piece, row, tile, sr)
+//   pol.out_row(piece, row)       row of `out`, or -1
+//   pol.record(piece)             null, or where this piece's partial results go (D x rows floats,
+//                                 column-major), and pol.record_ml(piece)
+template <int D, int PAIR, typename Pol>
+__device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
+    using Lay = Layout<D, PAIR>;
+    using Piece = typename Pol::Piece;
+    constexpr int HALVES = Lay::HALVES, kTile = Lay::TILE, NQ = Lay::NQ, ST = Lay::ST;
+    constexpr int kRecRows = kRows * (PAIR + 1);
+    const Barriers<D, PAIR> bar(sm);
+    volatile int *vabort = bar.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t limit = pol.timeout_ns;
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLowRegs));
+        if (warp == 8 || warp == 11) {
+            // ------------------------------------------------ TMA producers
+            const bool is_k = warp == 8;
+            uint64_t *full = is_k ? bar.k_full : bar.v_full, *empty = is_k ? bar.k_empty : bar.v_empty;
+            uint8_t *ring = sm + (is_k ? Lay::OFF_K : Lay::OFF_V);
+            typename Pol::Iter walk(pol, true);
+            Piece q;
+            bool ok = true;
+            int it = 0, piece = 0;
+            while (ok && walk.next(q)) {
+                const int n = q.tiles();
+                for (int j = 0; j < n && ok; ++j, ++it) {
+                    const int st = it % ST;
+                    const auto where = pol.kv_look(q, j, lane);
+                    if (__any_sync(0xffffffffu, *vabort != 0) || !warp_wait(&empty[st], ((it / ST) & 1) ^ 1, limit)) {
+                        if (lane == 0) set_status(pol.status, STATUS_TIMEOUT);
+                        *vabort = 1;
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], kTile);
+                    __syncwarp();
+                    pol.kv(q, j, where, is_k, ring + st * kTile, &full[st], lane);
+                    if (is_k && j == 0) {
+                        // the piece's query rows, into the buffer that the scores of NQ pieces ago released
+                        const int qb = piece % NQ;
+                        if (!warp_wait(&bar.q_empty[qb], ((piece / NQ) & 1) ^ 1, limit)) {
+                            if (lane == 0) set_status(pol.status, STATUS_TIMEOUT);
+                            *vabort = 1;
+                            ok = false;
+                        } else {
+                            if (lane == 0) {
+                                const int nh = PAIR && q.k1 > 0 ? 2 : 1;
+                                mbar_arrive_expect_tx(&bar.q_full[qb], nh * HALVES * pol.q_bytes());
+                                for (int hh = 0; hh < nh; ++hh)
+                                    pol.q(q, hh, sm + Lay::OFF_Q + (qb * (PAIR + 1) + hh) * kTile, &bar.q_full[qb]);
+                            }
+                            ++piece;
+                        }
+                        __syncwarp();
+                    }
+                }
+                walk.done();
+            }
+            // no copy is in flight when the CTA leaves, whatever the other warps did
+            for (int i = max(0, it - ST); i < it; ++i) warp_wait(&full[i % ST], (i / ST) & 1, limit);
+            if (is_k)
+                for (int i = max(0, piece - NQ); i < piece; ++i)
+                    warp_wait(&bar.q_full[i % NQ], (i / NQ) & 1, limit);
+        } else if (warp == 9) {
+            // ------------------------------------------------ MMA issuer
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128, false, false);
+                constexpr uint32_t idesc_o = tc::idesc_bf16(128, D, false, true);
+                bool issued = false, ok = true;
+                // (waits for P spin: a suspended thread resumed ~600 cycles late)
+                auto wait = [&](uint64_t *b, uint32_t par, bool spin = false) {
+                    if (!ok || *vabort || !(spin ? mbar_wait_spin(b, par, limit) : mbar_wait(b, par, limit))) {
+                        if (ok) set_status(pol.status, STATUS_TIMEOUT);
+                        ok = false;
+                        *vabort = 1;
+                    }
+                    return ok;
+                };
+                const uint64_t dq = tc::sdesc_sw128(smem_u32(sm + Lay::OFF_Q), 16, 1024);
+                const uint64_t dk = tc::sdesc_sw128(smem_u32(sm + Lay::OFF_K), 16, 1024);
+                const uint64_t dv = tc::sdesc_sw128(smem_u32(sm + Lay::OFF_V), kHalf, 1024);
+                // S block sb = Q tile qt times K stage ks: D / 16 K-steps over d_h
+                auto mma_s = [&](int sb, int qt, int ks) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                        tc::mma_ss(tmem + sb * 128, dq + ((qt * kTile) >> 4) + off, dk + ((ks * kTile) >> 4) + off,
+                                   idesc_s, kk > 0 ? 1u : 0u);
+                    }
+                    tc::commit(&bar.s_full[sb]);
+                    issued = true;
+                };
+                // O block sb += P block sb times V stage vs: two K-steps of 16 keys per chunk
+                auto mma_pv = [&](int sb, int vs, bool acc, bool split, int chunks) {
+                    if (chunks == 4 && !split) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            tc::mma_ts(tmem + 256 + sb * 128, tmem + sb * 128 + kk * 8,
+                                       dv + ((vs * kTile + kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
+                    } else {
+#pragma unroll 1
+                        for (int ps = 0; ps < (split ? 2 : 1); ++ps)
+#pragma unroll 1
+                            for (int kk = 0; kk < 2 * chunks; ++kk)
+                                tc::mma_ts(tmem + 256 + sb * 128, tmem + sb * 128 + ps * 64 + kk * 8,
+                                           dv + ((vs * kTile + kk * 2048) >> 4), idesc_o,
+                                           (acc || ps > 0 || kk > 0) ? 1u : 0u);
+                    }
+                };
+                // The scores run ahead of P.V (two tiles for PAIR = 0, one for PAIR = 1), across
+                // pieces: s_* is that walk, the loop below the one of P.V.
+                typename Pol::Iter sw(pol, false), vw(pol, false);
+                Piece sq, vq;
+                int s_it = 0, s_j = 0, s_n = 0, s_piece = -1, cnt0 = 0, cnt1 = 0, it = 0;
+                // the score walk's next tile, with its K and (for a piece's first) Q in place
+                auto s_next = [&]() {
+                    if (s_j == s_n) {
+                        if (!sw.next(sq)) return false;
+                        ++s_piece;
+                        s_j = 0;
+                        s_n = sq.tiles();
+                        if (!wait(&bar.q_full[s_piece % NQ], (s_piece / NQ) & 1)) return false;
+                    }
+                    return wait(&bar.k_full[s_it % ST], (s_it / ST) & 1);
+                };
+                // closes the tile: its K stage, and after a piece's last tile its Q buffer
+                auto s_close = [&]() {
+                    tc::commit(&bar.k_empty[s_it % ST]);
+                    if (++s_j == s_n) tc::commit(&bar.q_empty[s_piece % NQ]);
+                    ++s_it;
+                };
+                bool more;
+                if constexpr (!PAIR) {
+                    auto s_tile = [&]() {
+                        if (!s_next()) return false;
+                        mma_s(s_it & 1, s_piece % NQ, s_it % ST);
+                        s_close();
+                        return true;
+                    };
+                    more = s_tile() && s_tile();
+                    while (ok && vw.next(vq)) {
+                        const int n = vq.tiles();
+                        for (int j = 0; j < n && ok; ++j, ++it) {
+                            const int st = it % ST, sb = it & 1;
+                            if (!wait(&bar.v_full[st], (it / ST) & 1)) break;
+                            int &c = sb ? cnt1 : cnt0;
+                            if (!wait(&bar.p_ready[sb], c & 1, true)) break;
+                            ++c;
+                            tc::fence_after();
+                            mma_pv(sb, st, j >= 2, vq.split, chunks_of(vq.k0, j));
+                            tc::commit(&bar.v_empty[st]);
+                            if (j + 1 == n) {
+                                tc::commit(&bar.o_done[0]);
+                                tc::commit(&bar.o_done[1]);
+                            }
+                            if (more) more = s_tile();
+                        }
+                        vw.done();
+                    }
+                } else {
+                    more = s_next();
+                    if (more) {
+                        if (sq.k0 > 0) mma_s(0, (s_piece % NQ) * 2, 0);
+                        if (sq.k1 > 0) mma_s(1, (s_piece % NQ) * 2 + 1, 0);
+                        s_close();
+                    }
+                    while (ok && vw.next(vq)) {
+                        const int n = vq.tiles();
+                        for (int j = 0; j < n && ok; ++j, ++it) {
+                            const int st = it % ST;
+                            const bool on0 = vq.k0 > j * kKeys, on1 = vq.k1 > j * kKeys;
+                            if (!wait(&bar.v_full[st], (it / ST) & 1)) break;
+                            if (on0) {
+                                if (!wait(&bar.p_ready[0], cnt0++ & 1, true)) break;
+                                tc::fence_after();
+                                mma_pv(0, st, j > 0, vq.split, chunks_of(vq.k0, j));
+                            }
+                            more = more && s_next();
+                            if (!ok) break;
+                            if (more && sq.k0 > s_j * kKeys) mma_s(0, (s_piece % NQ) * 2, s_it % ST);
+                            if (on1) {
+                                if (!wait(&bar.p_ready[1], cnt1++ & 1, true)) break;
+                                tc::fence_after();
+                                mma_pv(1, st, j > 0, vq.split, chunks_of(vq.k1, j));
+                            }
+                            tc::commit(&bar.v_empty[st]);
+                            if (j + 1 == n) {
+                                if (vq.k0 > 0) tc::commit(&bar.o_done[0]);
+                                if (vq.k1 > 0) tc::commit(&bar.o_done[1]);
+                            }
+                            if (more) {
+                                if (sq.k1 > s_j * kKeys) mma_s(1, (s_piece % NQ) * 2 + 1, s_it % ST);
+                                s_close();
+                            }
+                        }
+                        vw.done();
+                    }
+                }
+                if (issued && !ok) {  // let MMAs already issued finish before TMEM is freed
+                    tc::commit(bar.drain);
+                    mbar_wait(bar.drain, 0, limit);
+                }
+            }
+            __syncwarp();
+        } else {
+            pol.side_warp(lane);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
+        // ------------------------------------------------ softmax + epilogue
+        const int hh = warp >> 2;          // row tile (PAIR) or key-tile parity
+        const int t = threadIdx.x & 127;   // row = tensor-memory lane
+        const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_off + hh * 128;
+        const uint32_t tO = tmem + lane_off + 256 + hh * 128;
+        float2 *ml = reinterpret_cast<float2 *>(sm + Lay::OFF_ML);
+        typename Pol::Iter walk(pol, true);
+        bool ok = true;
+        int it = 0, cnt = 0, piece = 0, met = 0;
+        auto both_meet = [&]() {  // bounded: false when the wait ran out
+            mbar_arrive(bar.meet);
+            return warp_wait(bar.meet, met++ & 1, limit);
+        };
+        Piece q;
+        bool have = walk.next(q);
+        typename Pol::Row row = {};
+        if (have) row = pol.row(q, PAIR ? hh : 0, t);
+        while (have) {
+            const int n = q.tiles(), keys = PAIR && hh ? q.k1 : q.k0;
+            float m = -INFINITY, l = 0.f;
+            bool first = true;
+            for (int j = 0; j < n; ++j, ++it) {
+                if (PAIR ? j * kKeys >= keys : (it & 1) != hh) continue;
+                const bool aborted = __any_sync(0xffffffffu, *vabort != 0);
+                if (aborted || !warp_wait(&bar.s_full[hh], cnt & 1, limit)) {
+                    ok = false;
+                    break;
+                }
+                ++cnt;
+                tc::fence_after();
+                const int nch = chunks_of(keys, j);
+                if (nch == 4 && !q.split && !pol.masked(q, row, j)) {
+                    softmax_step<D, true>(tS, tO, pol.scale_log2, first, false, 4, m, l, [](uint32_t(&)[4][32]) {});
+                } else {
+                    softmax_step<D, false>(tS, tO, pol.scale_log2, first, q.split, nch, m, l,
+                                           [&](uint32_t(&sr)[4][32]) { pol.mask(q, row, j, sr); });
+                    // V rows past the sequence's end: P is 0 there, but 0 times what they hold must
+                    // stay 0.  The first warpgroup that uses the tile clears them, ahead of its P.V;
+                    // the stage cannot be refilled before that.
+                    const int r0 = q.v_end - j * kKeys, r1 = 32 * chunks_of(max(q.k0, q.k1), j);
+                    if (r0 < r1 && (!PAIR || hh == 0 || q.k0 <= j * kKeys)) {
+                        if (!warp_wait(&bar.v_full[it % ST], (it / ST) & 1, limit)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t *tile = sm + Lay::OFF_V + (it % ST) * kTile;
+                        for (int i = t; i < (r1 - r0) * HALVES * 8; i += 128) {
+                            const int rr = r0 + i / (HALVES * 8), rem = i % (HALVES * 8);
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                             smem_u32(tile + (rem >> 3) * kHalf + rr * 128 + (rem & 7) * 16)),
+                                         "r"(0u)
+                                         : "memory");
+                        }
+                        fence_proxy_async_smem();
+                    }
+                }
+                first = false;
+                tc::fence_before();
+                mbar_arrive(&bar.p_ready[hh]);
+            }
+            if (!ok) break;
+            // the next piece's row is looked up while this one's last P.V runs
+            const Piece now = q;
+            const typename Pol::Row mine = row;
+            have = walk.next(q);
+            if (have) row = pol.row(q, PAIR ? hh : 0, t);
+            if (!PAIR || keys > 0) {
+                if (!warp_wait(&bar.o_done[hh], piece & 1, limit)) {
+                    ok = false;
+                    break;
+                }
+                ++piece;
+                tc::fence_after();
+            }
+            float *rec = pol.record(now);
+            // columns [c0, c0 + NC) of O, or of the merge of both parities' O
+            constexpr int NC = PAIR ? D : D / 2, CH = NC < 64 ? NC : 64;
+            float w0 = 1.f, w1 = 0.f, M = m, L = l;
+            uint32_t tA = tO;
+            int c0 = 0;
+            if constexpr (!PAIR) {
+                ml[hh * kRows + t] = make_float2(m, l);
+                if (!both_meet()) {
+                    ok = false;
+                    break;
+                }
+                const float2 a = ml[t], b = ml[kRows + t];
+                M = fmaxf(a.x, b.x);
+                w0 = a.x == -INFINITY ? 0.f : fast_exp2(a.x - M);
+                w1 = b.x == -INFINITY ? 0.f : fast_exp2(b.x - M);
+                L = w0 * a.y + w1 * b.y;
+                tA = tmem + lane_off + 256;
+                c0 = hh * NC;
+            }
+            if (!PAIR || keys > 0) {
+                const int out_row = pol.out_row(now, mine);
+                if (!rec) {
+                    const float inv = L > 0.f ? 1.f / L : 0.f;
+                    w0 *= inv;
+                    w1 *= inv;
+                }
+#pragma unroll 1
+                for (int c = c0; c < c0 + NC; c += CH) {
+                    uint32_t pk[CH / 2];
+#pragma unroll
+                    for (int cc = 0; cc < CH; cc += 32) {
+                        uint32_t oa[32], ob[32];
+                        tc::ld32(tA + c + cc, oa);
+                        if constexpr (!PAIR) tc::ld32(tA + 128 + c + cc, ob);
+                        tc::wait_ld();
+                        tc::hold32(oa);
+                        if constexpr (!PAIR) tc::hold32(ob);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            // (a parity without a key holds an O that was never written)
+                            float v0 = w0 != 0.f ? w0 * __uint_as_float(oa[e]) : 0.f;
+                            float v1 = w0 != 0.f ? w0 * __uint_as_float(oa[e + 1]) : 0.f;
+                            if constexpr (!PAIR) {
+                                v0 = w1 != 0.f ? fmaf(w1, __uint_as_float(ob[e]), v0) : v0;
+                                v1 = w1 != 0.f ? fmaf(w1, __uint_as_float(ob[e + 1]), v1) : v1;
+                            }
+                            if (rec) {
+                                // column-major: a warp's stores are 128 bytes in a row
+                                float *d = rec + (size_t)(c + cc + e) * kRecRows + (PAIR ? hh * kRows : 0) + t;
+                                if (out_row >= 0) {
+                                    d[0] = v0;
+                                    d[kRecRows] = v1;
+                                }
+                            }
+                            pk[(cc + e) / 2] = pack_bf16x2(v0, v1);
+                        }
+                    }
+                    if (!rec) store_rows<D, CH / 8>(pol.out, out_row, c, pk);
+                }
+                if (rec && (PAIR || hh == 0) && out_row >= 0)
+                    pol.record_ml(now)[(PAIR ? hh * kRows : 0) + t] = make_float2(M, L);
+            }
+            walk.done();
+            tc::fence_before();
+            if constexpr (!PAIR) {  // both have read both O before either is written again
+                if (!both_meet()) {
+                    ok = false;
+                    break;
+                }
+            }
+        }
+        if (!ok && lane == 0) {
+            set_status(pol.status, STATUS_TIMEOUT);
+            *vabort = 1;
+        }
+    }
+}
+
+// Exclusive sums cu[0..n) of f(i), and the whole in cu[n], by all kThreads
+// threads of the block; scratch holds 32 ints.  Ends with a barrier.
+template <typename F>
+__device__ __forceinline__ int block_prefix(int n, int *cu, int *scratch, F f) {
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int chunk = (n + kThreads - 1) / kThreads;
+    const int i0 = min(n, tid * chunk), i1 = min(n, i0 + chunk);
+    int local = 0;
+    for (int i = i0; i < i1; ++i) {
+        const int x = f(i);
+        cu[i] = x;
+        local += x;
+    }
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) scratch[wid] = incl;
+    __syncthreads();
+    int run = incl - local;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) run += w < wid ? scratch[w] : 0;
+    for (int i = i0; i < i1; ++i) {
+        const int x = cu[i];
+        cu[i] = run;
+        run += x;
+    }
+    if (tid == kThreads - 1) cu[n] = run;
+    __syncthreads();
+    return cu[n];
 }
 
 }  // namespace att

@@ -130,7 +130,7 @@ cudaError_t launch_pages_reserve(int32_t *table, int32_t *refcount, const int32_
                                  void *workspace, unsigned *status, cudaStream_t stream);
 
 // Causal attention over packed sequences (tcgen05).  tmq: [d_h, H, N] in boxes
-// of [64 dims x H/G heads x kPackRows / (H/G) positions]; tmk, tmv: [d_h, G, N]
+// of [64 dims x H/G heads x 128 / (H/G) positions]; tmk, tmv: [d_h, G, N]
 // in boxes of [64 x 1 x 128].
 struct PackedArgs {
     const int32_t *cu;
@@ -139,6 +139,7 @@ struct PackedArgs {
     int B, N, H, G, d_h;
     unsigned *status;
     uint64_t timeout_ns;
+    int num_sms;
     int window;
 };
 cudaError_t launch_prefill_packed(const PackedArgs &a, const CUtensorMap *tmq, const CUtensorMap *tmk,
@@ -161,7 +162,7 @@ struct TreeArgs {
     uint64_t timeout_ns;
     int num_sms;
 };
-size_t decode_tree_workspace(int B, int n, int r, int d_h, int num_sms);
+size_t decode_tree_workspace(int n, int r, int d_h, int num_sms);
 cudaError_t launch_decode_tree(const TreeArgs &a, const CUtensorMap *tmq, const CUtensorMap *tmk,
                                const CUtensorMap *tmv, cudaStream_t stream);
 
