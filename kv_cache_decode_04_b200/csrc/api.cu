@@ -597,6 +597,8 @@ int gqa_prefill_packed(const void *q, const void *k, const void *v, const int32_
     if ((long long)N * H >= (1ll << 31)) return fail(GQA_ERR_UNSUPPORTED, "N*H must be below 2^31");
     if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(out, 16) || misaligned(cu_seqlens, 4))
         return fail(GQA_ERR_ALIGN, "q, k, v and out must be 16-byte aligned");
+    if (((long long)N / (2 * (128 / (H / G))) + B + 1) * G >= (1ll << 30))
+        return fail(GQA_ERR_UNSUPPORTED, "too many query tiles for one call");
     const size_t qb = (size_t)N * H * d_h * 2, kb = (size_t)N * G * d_h * 2;
     if (overlaps(out, qb, q, qb) || overlaps(out, qb, k, kb) || overlaps(out, qb, v, kb) ||
         overlaps(out, qb, cu_seqlens, (size_t)(B + 1) * 4))

@@ -22,9 +22,12 @@
 // Roles (384 threads):
 //   warps 0-3, 4-7  softmax and epilogue of row tile / key parity 0, 1: one
 //                   thread per row = tensor-memory lane
-//   warp 8          K tiles and Q rows by TMA     warp 11  V tiles by TMA
-//   warp 9          allocates tensor memory; one lane issues every tcgen05.mma
-//   warp 10         the policy's (the packed prefill's work list)
+//   warp 8          K tiles and Q rows by TMA
+//   warp 11         V tiles by TMA, and what the policy has to do on the side
+//   warps 9, 10     tcgen05.mma of row tile / key parity 0, 1: one lane of each issues.
+//                   An issuing thread spends a third of a tile's time in checks of
+//                   barriers and on instructions between its MMAs; with two of them
+//                   one's MMAs fill the other's gaps.
 // Tensor memory: S0/P0, S1/P1 (128 columns each), O0, O1 (128 each).  P (bf16)
 // overwrites its S block; the S of a later tile is issued behind the P.V that
 // reads that P, and MMAs of one thread complete in order.
@@ -71,7 +74,7 @@ struct Layout {
     static constexpr int OFF_K = NQ * (PAIR + 1) * TILE;
     static constexpr int OFF_V = OFF_K + ST * TILE;
     static constexpr int OFF_BAR = OFF_V + ST * TILE;
-    static constexpr int OFF_ML = OFF_BAR + 384;              // [2][128] (m, l) of the two parities
+    static constexpr int OFF_ML = OFF_BAR + 400;              // [2][128] (m, l) of the two parities
     static constexpr int OFF_POLICY = OFF_ML + (PAIR ? 0 : 2 * 128 * 8);  // what the policy keeps
     static constexpr int SMEM = 1024 + OFF_POLICY;
 };
@@ -111,104 +114,108 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64
     return __all_sync(0xffffffffu, ok);
 }
 
-// One online-softmax step for this thread's query row (its tensor-memory lane):
-// reads the scores at tS, moves the running maximum m (log2 units) and the sum
-// l, and writes P = 2^(s - m) as bf16 pairs over the first 64 columns at tS.
+// Online softmax of this thread's query row (its tensor-memory lane) over one
+// tile of scores at tS: moves the running maximum m (log2 units) and the sum l
+// and writes P = 2^(s - m) as bf16 pairs over the scores.
 //   - The maximum moves (and O at tO is rescaled) only when it grows by more
 //     than 8, so p <= 2^8: numerator and denominator use the same stale one.
 //   - `first`: O holds nothing of this row yet.  Otherwise the P.V that last
 //     wrote O is complete, because the S just read was issued behind it.
 //   - m = -inf (no key seen yet): every score is -inf and p = 0.
-//   - PLAIN: a whole tile that every row sees.  Otherwise only the first 32 *
-//     nch columns are read and written, `mask(sr)` sets hidden scores to -inf,
-//     and with `split_p` P is carried as P_hi + P_lo, two bf16 terms (about 16
-//     significant bits), P_lo in columns 64..127: for rows that see so few keys
-//     that the rounding of P does not average out.
-// The row sum adds the unrounded p in fp32.
-template <int D, bool PLAIN, typename Mask>
-__device__ __forceinline__ void softmax_step(uint32_t tS, uint32_t tO, float scale_log2, bool first, bool split_p,
-                                             int nch, float &m, float &l, Mask mask) {
+//   - The row sum adds the unrounded p in fp32.
+// Moves the maximum to cover mx (raw scores; the scale is positive).
+template <int D>
+__device__ __forceinline__ void move_max(uint32_t tO, float mx, bool first, float &m, float &l) {
+    if (first) {
+        m = mx;
+        l = 0.f;
+        return;
+    }
+    const float mn = fmaxf(m, mx);
+    const bool need = mn > m + 8.f;
+    if (!__any_sync(0xffffffffu, need)) return;
+    float alpha = 1.f;
+    if (need) {
+        alpha = fast_exp2(m - mn);
+        m = mn;
+        l *= alpha;
+    }
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+        uint32_t orow[16];
+        tc::ld16(tO + c * 16, orow);
+        tc::wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) orow[e] = __float_as_uint(__uint_as_float(orow[e]) * alpha);
+        tc::st16(tO + c * 16, orow);
+    }
+}
+
+// exp of 32 raw scores and their sum in rs2 (four packed partial sums); bf16 pairs.
+__device__ __forceinline__ void exp_chunk(const uint32_t (&sr)[32], uint64_t sc2, uint64_t nm2, uint64_t (&rs2)[4],
+                                          uint64_t (*keep)[16], uint32_t (&pk)[16]) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const uint64_t x2 =
+            f32x2_fma(f32x2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), sc2, nm2);
+        float x0, x1;
+        f32x2_unpack(x2, x0, x1);
+        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+        const uint64_t p2 = f32x2_pack(p0, p1);
+        rs2[e & 3] = f32x2_add(rs2[e & 3], p2);
+        if (keep) (*keep)[e] = p2;
+        pk[e] = pack_bf16x2(p0, p1);
+    }
+}
+
+__device__ __forceinline__ float sum_of(const uint64_t (&rs2)[4]) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a0, a1;
+        f32x2_unpack(rs2[i], a0, a1);
+        sum += a0 + a1;
+    }
+    return sum;
+}
+
+__device__ __forceinline__ float max_chunk(const uint32_t (&sr)[32], float mx) {
+    float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(sr[e]));
+    return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+}
+
+// A whole tile that every row sees; P in columns [0, 64).
+template <int D>
+__device__ __forceinline__ void softmax_whole(uint32_t tS, uint32_t tO, float scale_log2, bool first, float &m,
+                                              float &l) {
     uint32_t sr[4][32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        if (PLAIN || c < nch) {
-            tc::ld32(tS + c * 32, sr[c]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) sr[c][e] = __float_as_uint(-INFINITY);
-        }
-    }
+    for (int c = 0; c < 4; ++c) tc::ld32(tS + c * 32, sr[c]);
     tc::wait_ld();
 #pragma unroll
     for (int c = 0; c < 4; ++c) tc::hold32(sr[c]);
-    if constexpr (!PLAIN) mask(sr);
-    // row maximum of the raw scores (the scale is positive), eight partial maxima
-    float mx8[8];
+    float mx4[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mx8[i] = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], __uint_as_float(sr[c][e]));
-    const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                           fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * scale_log2;
+    for (int c = 0; c < 4; ++c) mx4[c] = max_chunk(sr[c], -INFINITY);
+    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
+    const float m0 = first ? mx : m;
+    // (the rescale of O, when there is one, comes after P is written: P is what the tensor core waits for)
+    const float mn = first ? mx : fmaxf(m, mx);
+    const bool need = mn > m0 + 8.f;
+    const bool rescale = __any_sync(0xffffffffu, need);
     float alpha = 1.f;
-    bool rescale = false;
-    if (first) {
-        m = mx;
-    } else {
-        const float mn = fmaxf(m, mx);
-        const bool need = mn > m + 8.f;
-        rescale = __any_sync(0xffffffffu, need);
-        if (need) {
-            alpha = fast_exp2(m - mn);
-            m = mn;
-            l *= alpha;
-        }
-    }
+    if (need) alpha = fast_exp2(m0 - mn);
+    m = need ? mn : m0;
     const float mu = m == -INFINITY ? 0.f : m;
     const uint64_t sc2 = f32x2_pack(scale_log2, scale_log2), nm2 = f32x2_pack(-mu, -mu);
     uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
-    if (PLAIN || !split_p) {
 #pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-            if (!PLAIN && c4 >= nch) continue;
-            uint32_t pk[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const uint64_t x2 = f32x2_fma(
-                    f32x2_pack(__uint_as_float(sr[c4][2 * e]), __uint_as_float(sr[c4][2 * e + 1])), sc2, nm2);
-                float x0, x1;
-                f32x2_unpack(x2, x0, x1);
-                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                rs2[e & 3] = f32x2_add(rs2[e & 3], f32x2_pack(p0, p1));
-                pk[e] = pack_bf16x2(p0, p1);
-            }
-            tc::st16(tS + c4 * 16, pk);
-        }
-    } else {
-        // P_lo of chunk c4 goes to columns 64 + 16 c4, which chunks 2 and 3 of S
-        // occupied: their scores are in registers by now
-#pragma unroll
-        for (int c4 = 0; c4 < 4; ++c4) {
-            if (c4 >= nch) continue;
-#pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4) {
-                uint32_t ph[4], pl[4];
-#pragma unroll
-                for (int e1 = 0; e1 < 4; ++e1) {
-                    const int e = e4 * 4 + e1;
-                    const float p0 = fast_exp2(fmaf(__uint_as_float(sr[c4][2 * e]), scale_log2, -mu));
-                    const float p1 = fast_exp2(fmaf(__uint_as_float(sr[c4][2 * e + 1]), scale_log2, -mu));
-                    rs2[e1] = f32x2_add(rs2[e1], f32x2_pack(p0, p1));
-                    ph[e1] = pack_bf16x2(p0, p1);
-                    const float2 h = unpack_bf16x2(ph[e1]);
-                    pl[e1] = pack_bf16x2(p0 - h.x, p1 - h.y);
-                }
-                tc::st4(tS + c4 * 16 + e4 * 4, ph);
-                tc::st4(tS + 64 + c4 * 16 + e4 * 4, pl);
-            }
-        }
+    for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+        exp_chunk(sr[c], sc2, nm2, rs2, nullptr, pk);
+        tc::st16(tS + c * 16, pk);
     }
     if (rescale) {
 #pragma unroll 1
@@ -221,14 +228,61 @@ __device__ __forceinline__ void softmax_step(uint32_t tS, uint32_t tO, float sca
             tc::st16(tO + c * 16, orow);
         }
     }
-    float sum = 0.f;
+    l = (first ? 0.f : l * alpha) + sum_of(rs2);
+    tc::wait_st();
+}
+
+// Any other tile: only its first 32 * nch keys, of which bit e of words(c)
+// says whether the row sees key 32 c + e.  P of chunk c stays in the chunk's
+// own 32 columns: P_hi in the first 16 and, with `split`, P_lo = p - P_hi in
+// the next 16 (two bf16 terms, about 16 significant bits: for rows that see so
+// few keys that the rounding of P does not average out).  Two passes over the
+// chunks in a rolled loop: a short tile costs what it holds, and the code stays
+// small (unrolled, these paths were 38 KB of instructions, which every launch
+// fetched anew).
+template <int D, typename Words>
+__device__ __forceinline__ void softmax_part(uint32_t tS, uint32_t tO, float scale_log2, bool first, bool split,
+                                             int nch, float &m, float &l, Words words) {
+    auto load = [&](int c, uint32_t (&sr)[32]) {
+        tc::ld32(tS + c * 32, sr);
+        const uint32_t w = words(c);
+        tc::wait_ld();
+        tc::hold32(sr);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a0, a1;
-        f32x2_unpack(rs2[i], a0, a1);
-        sum += a0 + a1;
+        for (int e = 0; e < 32; ++e)
+            if (!((w >> e) & 1u)) sr[e] = __float_as_uint(-INFINITY);
+    };
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < nch; ++c) {
+        uint32_t sr[32];
+        load(c, sr);
+        mx = max_chunk(sr, mx);
     }
-    l = first ? sum : l + sum;
+    move_max<D>(tO, mx * scale_log2, first, m, l);
+    const float mu = m == -INFINITY ? 0.f : m;
+    const uint64_t sc2 = f32x2_pack(scale_log2, scale_log2), nm2 = f32x2_pack(-mu, -mu);
+    uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 1
+    for (int c = 0; c < nch; ++c) {
+        uint32_t sr[32], pk[16];
+        uint64_t p2[16];
+        load(c, sr);
+        exp_chunk(sr, sc2, nm2, rs2, &p2, pk);
+        tc::st16(tS + c * 32, pk);
+        if (split) {
+            const uint64_t minus1 = f32x2_pack(-1.f, -1.f);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {  // p - P_hi is exact in fp32
+                const uint64_t hi = f32x2_pack(__uint_as_float(pk[e] << 16), __uint_as_float(pk[e] & 0xffff0000u));
+                float r0, r1;
+                f32x2_unpack(f32x2_fma(hi, minus1, p2[e]), r0, r1);
+                pk[e] = pack_bf16x2(r0, r1);
+            }
+            tc::st16(tS + c * 32 + 16, pk);
+        }
+    }
+    l += sum_of(rs2);
     tc::wait_st();
 }
 
@@ -283,14 +337,20 @@ __device__ __forceinline__ int chunks_of(int keys, int j) {  // 32-key chunks of
 template <int D, int PAIR>
 struct Barriers {
     static constexpr int ST = Layout<D, PAIR>::ST;
+    // Arrivals that release a K or V stage: both issuers use every tile of a pair
+    // (one that has nothing to do with a tile arrives without an MMA), one uses a
+    // tile otherwise.
+    static constexpr int USERS = PAIR ? 2 : 1;
     uint64_t *q_full, *q_empty;                          // [2] (NQ used)
     uint64_t *k_full, *k_empty, *v_full, *v_empty;       // [ST]
     uint64_t *s_full, *p_ready;                          // [2] per softmax warpgroup
-    // [2] a piece's last P.V is complete.  One per softmax warpgroup, committed only for
-    // pieces in which it has rows: no later phase can complete before it has seen this one.
+    // [2] a piece's last P.V of row tile / parity i is complete; only for pieces that have
+    // one.  No later phase can complete before both warpgroups have seen this one, since it
+    // takes a P that warpgroup i writes after this piece's epilogue.
     uint64_t *o_done;
     uint64_t *meet;                                      // the two warpgroups (PAIR = 0)
-    uint64_t *drain;
+    uint64_t *drain;                                     // [2] one per issuer
+    uint64_t *turn;                                      // [2] issuer i may go on
     uint64_t *policy;                                    // [16]
     uint32_t *tmem_slot;
     int *abort_flag;
@@ -302,7 +362,7 @@ struct Barriers {
         p_ready = b + 6;
         o_done = b + 8;
         meet = b + 10;
-        drain = b + 11;
+        drain = b + 46;
         k_full = b + 12;
         k_empty = k_full + ST;
         v_full = k_empty + ST;
@@ -310,23 +370,25 @@ struct Barriers {
         policy = b + 28;
         tmem_slot = reinterpret_cast<uint32_t *>(b + 44);
         abort_flag = reinterpret_cast<int *>(b + 45);
+        turn = b + 48;
     }
     __device__ void init() const {  // one thread
         for (int s = 0; s < 2; ++s) {
             mbar_init(&q_full[s], 1);
-            mbar_init(&q_empty[s], 1);
+            mbar_init(&q_empty[s], 2);
+            mbar_init(&drain[s], 1);
+            mbar_init(&turn[s], 1);
             mbar_init(&s_full[s], 1);
             mbar_init(&p_ready[s], 128);
             mbar_init(&o_done[s], 1);
         }
         for (int s = 0; s < ST; ++s) {
             mbar_init(&k_full[s], 1);
-            mbar_init(&k_empty[s], 1);
+            mbar_init(&k_empty[s], USERS);
             mbar_init(&v_full[s], 1);
-            mbar_init(&v_empty[s], 1);
+            mbar_init(&v_empty[s], USERS);
         }
         mbar_init(meet, 256);
-        mbar_init(drain, 1);
         *abort_flag = 0;
     }
 };
@@ -340,8 +402,10 @@ struct Barriers {
 //   pol.kv(piece, tile, K or V, stage address, barrier, lane)  loads of a tile, by a whole warp
 //   pol.kv_look(piece, tile, lane)  what kv() needs from memory, asked for before the stage is free
 //   pol.q(piece, row tile, address, barrier)  loads of Q rows, by one lane; pol.q_bytes() each
-//   pol.row(piece, row tile, row)  -> Pol::Row, the thread's row;  pol.masked(piece, row, tile)
-//   pol.mask(piece, row, tile, sr)
+//   pol.masked(piece, row tile, tile)  whether some row does not see all of a key tile
+//   pol.row(piece, row tile, row)  -> Pol::Row, the thread's row
+//   pol.words(piece, row, tile, c)  what the row sees of the 32 keys of chunk c, as bits
+//   pol.side(lane)                called by warp 11 before each of its pieces
 //   pol.out_row(piece, row)       row of `out`, or -1
 //   pol.record(piece)             null, or where this piece's partial results go (D x rows floats,
 //                                 column-major), and pol.record_ml(piece)
@@ -367,7 +431,9 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
             Piece q;
             bool ok = true;
             int it = 0, piece = 0;
-            while (ok && walk.next(q)) {
+            for (;;) {
+                if (!is_k) pol.side(lane);
+                if (!ok || !walk.next(q)) break;
                 const int n = q.tiles();
                 for (int j = 0; j < n && ok; ++j, ++it) {
                     const int st = it % ST;
@@ -407,150 +473,138 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
             if (is_k)
                 for (int i = max(0, piece - NQ); i < piece; ++i)
                     warp_wait(&bar.q_full[i % NQ], (i / NQ) & 1, limit);
-        } else if (warp == 9) {
-            // ------------------------------------------------ MMA issuer
-            if (lane == 0) {
-                constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128, false, false);
-                constexpr uint32_t idesc_o = tc::idesc_bf16(128, D, false, true);
-                bool issued = false, ok = true;
-                // (waits for P spin: a suspended thread resumed ~600 cycles late)
-                auto wait = [&](uint64_t *b, uint32_t par, bool spin = false) {
-                    if (!ok || *vabort || !(spin ? mbar_wait_spin(b, par, limit) : mbar_wait(b, par, limit))) {
-                        if (ok) set_status(pol.status, STATUS_TIMEOUT);
-                        ok = false;
-                        *vabort = 1;
+        } else if (lane == 0) {
+            // ------------------------------------------------ MMA issuers, warps 9 and 10
+            const int hh = warp - 9;
+            constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128, false, false);
+            constexpr uint32_t idesc_o = tc::idesc_bf16(128, D, false, true);
+            bool issued = false, ok = true;
+            // Spins (a suspended thread resumed ~600 cycles late); the abort flag and the time are
+            // looked at only while there is something to wait for.
+            auto wait = [&](uint64_t *b, uint32_t par) {
+                if (mbar_test_wait(b, par)) return true;
+                const uint64_t t0 = global_timer_ns();
+                for (;;) {
+                    for (int i = 0; i < 64; ++i)
+                        if (mbar_test_wait(b, par)) return true;
+                    if (*vabort || global_timer_ns() - t0 > limit) break;
+                }
+                set_status(pol.status, STATUS_TIMEOUT);
+                ok = false;
+                *vabort = 1;
+                return false;
+            };
+            const uint64_t dq = tc::sdesc_sw128(smem_u32(sm + Lay::OFF_Q), 16, 1024);
+            const uint64_t dk = tc::sdesc_sw128(smem_u32(sm + Lay::OFF_K), 16, 1024);
+            const uint64_t dv = tc::sdesc_sw128(smem_u32(sm + Lay::OFF_V), kHalf, 1024);
+            const uint32_t tS = tmem + hh * 128, tO = tmem + 256 + hh * 128;
+            // Two walks over the tiles: the scores' runs ahead of P.V's by LOOK tiles, across
+            // pieces.  Round k issues P.V of tile k - LOOK and S of tile k, where they are this
+            // issuer's.  What the round needs is looked up and waited for before its wait for P:
+            // from there to the S is on every tile's critical path.
+            // The issuers take turns, a group [P.V of one tile, S of the next] each.  Left to
+            // themselves they fall into step: both softmaxes then share the SM's issue slots, both
+            // groups the tensor core, and neither overlaps the other (4,800 cycles a tile of a pair
+            // against 3,990; passing the turn on before the S took 4,300, one thread for both row
+            // tiles 4,400).
+            constexpr int LOOK = PAIR ? 1 : 2;
+            typename Pol::Iter sw(pol, false), vw(pol, false);
+            Piece sq, vq;
+            int s_j = 0, s_n = 0, s_piece = -1, v_j = 0, v_n = 0, cnt = 0, turns = 0;
+            bool more = true;
+            for (int k = 0; ok; ++k) {
+                const int it = k - LOOK, vs = it & (ST - 1), ks = k & (ST - 1);
+                bool pv = it >= 0, mine = false, last = false;
+                int nch = 0;
+                if (pv) {
+                    if (v_j == v_n) {
+                        if (!vw.next(vq)) break;
+                        v_j = 0;
+                        v_n = vq.tiles();
                     }
-                    return ok;
-                };
-                const uint64_t dq = tc::sdesc_sw128(smem_u32(sm + Lay::OFF_Q), 16, 1024);
-                const uint64_t dk = tc::sdesc_sw128(smem_u32(sm + Lay::OFF_K), 16, 1024);
-                const uint64_t dv = tc::sdesc_sw128(smem_u32(sm + Lay::OFF_V), kHalf, 1024);
-                // S block sb = Q tile qt times K stage ks: D / 16 K-steps over d_h
-                auto mma_s = [&](int sb, int qt, int ks) {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                        tc::mma_ss(tmem + sb * 128, dq + ((qt * kTile) >> 4) + off, dk + ((ks * kTile) >> 4) + off,
-                                   idesc_s, kk > 0 ? 1u : 0u);
-                    }
-                    tc::commit(&bar.s_full[sb]);
-                    issued = true;
-                };
-                // O block sb += P block sb times V stage vs: two K-steps of 16 keys per chunk
-                auto mma_pv = [&](int sb, int vs, bool acc, bool split, int chunks) {
-                    if (chunks == 4 && !split) {
+                    const int keys = PAIR && hh ? vq.k1 : vq.k0;
+                    mine = PAIR ? keys > v_j * kKeys : (it & 1) == hh;
+                    last = PAIR ? keys <= (v_j + 1) * kKeys : v_j + 2 >= v_n;
+                    // how P lies in its S block: 0 as softmax_whole left it, else softmax_part's chunks
+                    nch = chunks_of(keys, v_j);
+                    if (nch == 4 && !vq.split && !pol.masked(vq, PAIR ? hh : 0, v_j)) nch = 0;
+                    if ((PAIR || mine) && !wait(&bar.v_full[vs], (it / ST) & 1)) break;
+                }
+                // the next scores, unless they open a piece: its Q may still be on its way, and
+                // P.V does not wait for that
+                bool s_ready = more && s_j < s_n;
+                const bool act = PAIR || (k & 1) == hh;  // this issuer's round
+                if (s_ready && act && !wait(&bar.k_full[ks], (k / ST) & 1)) break;
+                if (mine && !wait(&bar.p_ready[hh], cnt++ & 1)) break;
+                if (act && (hh == 1 || turns > 0) && !wait(&bar.turn[hh], (turns - 1 + hh) & 1)) break;
+                if (mine) {
+                    tc::fence_after();
+                    const uint64_t d = dv + ((vs * kTile) >> 4);
+                    const bool acc = PAIR ? v_j > 0 : v_j >= 2;
+                    // O += P V, two K-steps of 16 keys per chunk
+                    if (nch == 0) {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
-                            tc::mma_ts(tmem + 256 + sb * 128, tmem + sb * 128 + kk * 8,
-                                       dv + ((vs * kTile + kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
+                            tc::mma_ts(tO, tS + kk * 8, d + ((kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
                     } else {
 #pragma unroll 1
-                        for (int ps = 0; ps < (split ? 2 : 1); ++ps)
+                        for (int lo = 0; lo <= (vq.split ? 16 : 0); lo += 16)
 #pragma unroll 1
-                            for (int kk = 0; kk < 2 * chunks; ++kk)
-                                tc::mma_ts(tmem + 256 + sb * 128, tmem + sb * 128 + ps * 64 + kk * 8,
-                                           dv + ((vs * kTile + kk * 2048) >> 4), idesc_o,
-                                           (acc || ps > 0 || kk > 0) ? 1u : 0u);
+                            for (int kk = 0; kk < 2 * nch; ++kk)
+                                tc::mma_ts(tO, tS + (kk >> 1) * 32 + (kk & 1) * 8 + lo, d + ((kk * 2048) >> 4),
+                                           idesc_o, (acc || lo > 0 || kk > 0) ? 1u : 0u);
                     }
-                };
-                // The scores run ahead of P.V (two tiles for PAIR = 0, one for PAIR = 1), across
-                // pieces: s_* is that walk, the loop below the one of P.V.
-                typename Pol::Iter sw(pol, false), vw(pol, false);
-                Piece sq, vq;
-                int s_it = 0, s_j = 0, s_n = 0, s_piece = -1, cnt0 = 0, cnt1 = 0, it = 0;
-                // the score walk's next tile, with its K and (for a piece's first) Q in place
-                auto s_next = [&]() {
-                    if (s_j == s_n) {
-                        if (!sw.next(sq)) return false;
+                    if (last) tc::commit(&bar.o_done[hh]);
+                }
+                // S = Q K^T of tile k: D / 16 K-steps over d_h.  A piece's first one comes after the
+                // turn is passed on, since it may have to wait.
+                const bool opens = !s_ready;
+                if (opens) {
+                    if (act) mbar_arrive(&bar.turn[hh ^ 1]);
+                    if (more) more = sw.next(sq);
+                    if (more) {
                         ++s_piece;
                         s_j = 0;
                         s_n = sq.tiles();
-                        if (!wait(&bar.q_full[s_piece % NQ], (s_piece / NQ) & 1)) return false;
-                    }
-                    return wait(&bar.k_full[s_it % ST], (s_it / ST) & 1);
-                };
-                // closes the tile: its K stage, and after a piece's last tile its Q buffer
-                auto s_close = [&]() {
-                    tc::commit(&bar.k_empty[s_it % ST]);
-                    if (++s_j == s_n) tc::commit(&bar.q_empty[s_piece % NQ]);
-                    ++s_it;
-                };
-                bool more;
-                if constexpr (!PAIR) {
-                    auto s_tile = [&]() {
-                        if (!s_next()) return false;
-                        mma_s(s_it & 1, s_piece % NQ, s_it % ST);
-                        s_close();
-                        return true;
-                    };
-                    more = s_tile() && s_tile();
-                    while (ok && vw.next(vq)) {
-                        const int n = vq.tiles();
-                        for (int j = 0; j < n && ok; ++j, ++it) {
-                            const int st = it % ST, sb = it & 1;
-                            if (!wait(&bar.v_full[st], (it / ST) & 1)) break;
-                            int &c = sb ? cnt1 : cnt0;
-                            if (!wait(&bar.p_ready[sb], c & 1, true)) break;
-                            ++c;
-                            tc::fence_after();
-                            mma_pv(sb, st, j >= 2, vq.split, chunks_of(vq.k0, j));
-                            tc::commit(&bar.v_empty[st]);
-                            if (j + 1 == n) {
-                                tc::commit(&bar.o_done[0]);
-                                tc::commit(&bar.o_done[1]);
-                            }
-                            if (more) more = s_tile();
-                        }
-                        vw.done();
-                    }
-                } else {
-                    more = s_next();
-                    if (more) {
-                        if (sq.k0 > 0) mma_s(0, (s_piece % NQ) * 2, 0);
-                        if (sq.k1 > 0) mma_s(1, (s_piece % NQ) * 2 + 1, 0);
-                        s_close();
-                    }
-                    while (ok && vw.next(vq)) {
-                        const int n = vq.tiles();
-                        for (int j = 0; j < n && ok; ++j, ++it) {
-                            const int st = it % ST;
-                            const bool on0 = vq.k0 > j * kKeys, on1 = vq.k1 > j * kKeys;
-                            if (!wait(&bar.v_full[st], (it / ST) & 1)) break;
-                            if (on0) {
-                                if (!wait(&bar.p_ready[0], cnt0++ & 1, true)) break;
-                                tc::fence_after();
-                                mma_pv(0, st, j > 0, vq.split, chunks_of(vq.k0, j));
-                            }
-                            more = more && s_next();
-                            if (!ok) break;
-                            if (more && sq.k0 > s_j * kKeys) mma_s(0, (s_piece % NQ) * 2, s_it % ST);
-                            if (on1) {
-                                if (!wait(&bar.p_ready[1], cnt1++ & 1, true)) break;
-                                tc::fence_after();
-                                mma_pv(1, st, j > 0, vq.split, chunks_of(vq.k1, j));
-                            }
-                            tc::commit(&bar.v_empty[st]);
-                            if (j + 1 == n) {
-                                if (vq.k0 > 0) tc::commit(&bar.o_done[0]);
-                                if (vq.k1 > 0) tc::commit(&bar.o_done[1]);
-                            }
-                            if (more) {
-                                if (sq.k1 > s_j * kKeys) mma_s(1, (s_piece % NQ) * 2 + 1, s_it % ST);
-                                s_close();
-                            }
-                        }
-                        vw.done();
+                        if (!wait(&bar.q_full[s_piece % NQ], (s_piece / NQ) & 1)) break;
+                        if (act && !wait(&bar.k_full[ks], (k / ST) & 1)) break;
+                        s_ready = true;
                     }
                 }
-                if (issued && !ok) {  // let MMAs already issued finish before TMEM is freed
-                    tc::commit(bar.drain);
-                    mbar_wait(bar.drain, 0, limit);
+                if (s_ready) {
+                    const bool on = PAIR ? (hh ? sq.k1 : sq.k0) > s_j * kKeys : act;
+                    if (on) {
+                        const uint64_t q = dq + ((((s_piece % NQ) * (PAIR + 1) + (PAIR ? hh : 0)) * kTile) >> 4);
+                        const uint64_t kd = dk + ((ks * kTile) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                            tc::mma_ss(tS, q + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+                        }
+                        tc::commit(&bar.s_full[hh]);
+                        issued = true;
+                        tc::commit(&bar.k_empty[ks]);
+                    } else if (PAIR) {
+                        mbar_arrive(&bar.k_empty[ks]);
+                    }
+                    if (++s_j == s_n) tc::commit(&bar.q_empty[s_piece % NQ]);
+                }
+                if (act) {
+                    if (!opens) mbar_arrive(&bar.turn[hh ^ 1]);
+                    ++turns;
+                }
+                if (pv) {
+                    if (mine) tc::commit(&bar.v_empty[vs]);
+                    else if (PAIR) mbar_arrive(&bar.v_empty[vs]);
+                    if (++v_j == v_n) vw.done();
                 }
             }
-            __syncwarp();
-        } else {
-            pol.side_warp(lane);
+            if (issued && !ok) {  // let MMAs already issued finish before TMEM is freed
+                tc::commit(&bar.drain[hh]);
+                mbar_wait(&bar.drain[hh], 0, limit);
+            }
         }
+        __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kHighRegs));
         // ------------------------------------------------ softmax + epilogue
@@ -562,72 +616,25 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
         float2 *ml = reinterpret_cast<float2 *>(sm + Lay::OFF_ML);
         typename Pol::Iter walk(pol, true);
         bool ok = true;
-        int it = 0, cnt = 0, piece = 0, met = 0;
+        int it = 0, cnt = 0, met = 0, now_it = 0, now_n = 0;
+        int done[2] = {0, 0};  // pieces seen through o_done
         auto both_meet = [&]() {  // bounded: false when the wait ran out
             mbar_arrive(bar.meet);
             return warp_wait(bar.meet, met++ & 1, limit);
         };
-        Piece q;
-        bool have = walk.next(q);
-        typename Pol::Row row = {};
-        if (have) row = pol.row(q, PAIR ? hh : 0, t);
-        while (have) {
-            const int n = q.tiles(), keys = PAIR && hh ? q.k1 : q.k0;
-            float m = -INFINITY, l = 0.f;
-            bool first = true;
-            for (int j = 0; j < n; ++j, ++it) {
-                if (PAIR ? j * kKeys >= keys : (it & 1) != hh) continue;
-                const bool aborted = __any_sync(0xffffffffu, *vabort != 0);
-                if (aborted || !warp_wait(&bar.s_full[hh], cnt & 1, limit)) {
+        // Writes a piece's output, or its partial record; sets ok when a wait runs out.
+        auto epilogue = [&](const Piece &now, const typename Pol::Row &mine, float m, float l) {
+            const int keys = PAIR && hh ? now.k1 : now.k0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                // the row tile's own last P.V, or both parities' where the piece has them
+                if (PAIR ? i != hh || keys == 0 : now_n < 2 && (now_it & 1) != i) continue;
+                if (!warp_wait(&bar.o_done[i], done[i]++ & 1, limit)) {
                     ok = false;
-                    break;
+                    return;
                 }
-                ++cnt;
-                tc::fence_after();
-                const int nch = chunks_of(keys, j);
-                if (nch == 4 && !q.split && !pol.masked(q, row, j)) {
-                    softmax_step<D, true>(tS, tO, pol.scale_log2, first, false, 4, m, l, [](uint32_t(&)[4][32]) {});
-                } else {
-                    softmax_step<D, false>(tS, tO, pol.scale_log2, first, q.split, nch, m, l,
-                                           [&](uint32_t(&sr)[4][32]) { pol.mask(q, row, j, sr); });
-                    // V rows past the sequence's end: P is 0 there, but 0 times what they hold must
-                    // stay 0.  The first warpgroup that uses the tile clears them, ahead of its P.V;
-                    // the stage cannot be refilled before that.
-                    const int r0 = q.v_end - j * kKeys, r1 = 32 * chunks_of(max(q.k0, q.k1), j);
-                    if (r0 < r1 && (!PAIR || hh == 0 || q.k0 <= j * kKeys)) {
-                        if (!warp_wait(&bar.v_full[it % ST], (it / ST) & 1, limit)) {
-                            ok = false;
-                            break;
-                        }
-                        uint8_t *tile = sm + Lay::OFF_V + (it % ST) * kTile;
-                        for (int i = t; i < (r1 - r0) * HALVES * 8; i += 128) {
-                            const int rr = r0 + i / (HALVES * 8), rem = i % (HALVES * 8);
-                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
-                                             smem_u32(tile + (rem >> 3) * kHalf + rr * 128 + (rem & 7) * 16)),
-                                         "r"(0u)
-                                         : "memory");
-                        }
-                        fence_proxy_async_smem();
-                    }
-                }
-                first = false;
-                tc::fence_before();
-                mbar_arrive(&bar.p_ready[hh]);
             }
-            if (!ok) break;
-            // the next piece's row is looked up while this one's last P.V runs
-            const Piece now = q;
-            const typename Pol::Row mine = row;
-            have = walk.next(q);
-            if (have) row = pol.row(q, PAIR ? hh : 0, t);
-            if (!PAIR || keys > 0) {
-                if (!warp_wait(&bar.o_done[hh], piece & 1, limit)) {
-                    ok = false;
-                    break;
-                }
-                ++piece;
-                tc::fence_after();
-            }
+            tc::fence_after();
             float *rec = pol.record(now);
             // columns [c0, c0 + NC) of O, or of the merge of both parities' O
             constexpr int NC = PAIR ? D : D / 2, CH = NC < 64 ? NC : 64;
@@ -638,7 +645,7 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
                 ml[hh * kRows + t] = make_float2(m, l);
                 if (!both_meet()) {
                     ok = false;
-                    break;
+                    return;
                 }
                 const float2 a = ml[t], b = ml[kRows + t];
                 M = fmaxf(a.x, b.x);
@@ -694,11 +701,67 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
             walk.done();
             tc::fence_before();
             if constexpr (!PAIR) {  // both have read both O before either is written again
-                if (!both_meet()) {
+                if (!both_meet()) ok = false;
+            }
+        };
+        Piece q, now;
+        typename Pol::Row row = {}, mine = {};
+        float m = -INFINITY, l = 0.f;
+        bool open = false;  // `now` waits for its epilogue
+        while (ok) {
+            // the next piece and its row are looked up while the last P.V of the one before runs
+            const bool have = walk.next(q);
+            if (have) row = pol.row(q, PAIR ? hh : 0, t);
+            if (open) epilogue(now, mine, m, l);
+            open = have && ok;
+            if (!open) break;
+            const int n = q.tiles(), keys = PAIR && hh ? q.k1 : q.k0;
+            now_it = it;
+            now_n = n;
+            m = -INFINITY;
+            l = 0.f;
+            bool first = true;
+            for (int j = 0; j < n; ++j, ++it) {
+                if (PAIR ? j * kKeys >= keys : (it & 1) != hh) continue;
+                const bool aborted = __any_sync(0xffffffffu, *vabort != 0);
+                if (aborted || !warp_wait(&bar.s_full[hh], cnt & 1, limit)) {
                     ok = false;
                     break;
                 }
+                ++cnt;
+                tc::fence_after();
+                const int nch = chunks_of(keys, j);
+                if (nch == 4 && !q.split && !pol.masked(q, PAIR ? hh : 0, j)) {
+                    softmax_whole<D>(tS, tO, pol.scale_log2, first, m, l);
+                } else {
+                    softmax_part<D>(tS, tO, pol.scale_log2, first, q.split, nch, m, l,
+                                    [&](int c) { return pol.words(q, row, j, c); });
+                    // V rows past the sequence's end: P is 0 there, but 0 times what they hold must
+                    // stay 0.  Each warpgroup clears those that its P.V reads, ahead of it (both may
+                    // write zeros over zeros); the stage cannot be refilled before that P.V.
+                    const int r0 = q.v_end - j * kKeys, r1 = 32 * nch;
+                    if (r0 < r1) {
+                        if (!warp_wait(&bar.v_full[it % ST], (it / ST) & 1, limit)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t *tile = sm + Lay::OFF_V + (it % ST) * kTile;
+                        for (int i = t; i < (r1 - r0) * HALVES * 8; i += 128) {
+                            const int rr = r0 + i / (HALVES * 8), rem = i % (HALVES * 8);
+                            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                             smem_u32(tile + (rem >> 3) * kHalf + rr * 128 + (rem & 7) * 16)),
+                                         "r"(0u)
+                                         : "memory");
+                        }
+                        fence_proxy_async_smem();
+                    }
+                }
+                first = false;
+                tc::fence_before();
+                mbar_arrive(&bar.p_ready[hh]);
             }
+            now = q;
+            mine = row;
         }
         if (!ok && lane == 0) {
             set_status(pol.status, STATUS_TIMEOUT);

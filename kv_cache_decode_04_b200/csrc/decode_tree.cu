@@ -45,7 +45,7 @@ using namespace att;
 // the first cut: its sequence (-1: no such segment), KV head, row block, last
 // share, and the length of the whole line.
 struct Cut {
-    int b, g, rb, last, W, pad[3];
+    int b, g, rb, last, W, nd, pad[2];  // nd: drafts of the sequence
 };
 
 struct TreeParams {
@@ -70,7 +70,7 @@ struct TreeParams {
 // Tiles that a segment counts beyond its own.  A piece costs about 3.5 us
 // beside its tiles of 1.3 us (one row tile), and less against tiles of 2.3 us.
 template <int PAIR>
-constexpr int kSegCost = PAIR ? 1 : 2;
+constexpr int kSegCost = PAIR ? 1 : 3;
 
 // Cached positions and drafts of sequence b, forced into range.
 __device__ __forceinline__ int2 seq_state(const TreeParams &p, int b, bool *bad = nullptr) {
@@ -206,16 +206,9 @@ struct TreePolicy {
         }
         return w;
     }
-    __device__ bool masked(const Piece &q, const Row &, int j) const { return (q.j0 + j + 1) * kKeys > q.T; }
-    __device__ void mask(const Piece &q, const Row &w, int j, uint32_t (&sr)[4][32]) const {
-        const int rel = (q.j0 + j) * kKeys - q.T;  // the tile's first key, from the first draft
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint32_t word = visible_word(w.bits, rel + c * 32);
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-                if (!((word >> e) & 1u)) sr[c][e] = __float_as_uint(-INFINITY);
-        }
+    __device__ bool masked(const Piece &q, int, int j) const { return (q.j0 + j + 1) * kKeys > q.T; }
+    __device__ uint32_t words(const Piece &q, const Row &w, int j, int c) const {
+        return visible_word(w.bits, (q.j0 + j) * kKeys + c * 32 - q.T);
     }
     __device__ int out_row(const Piece &, const Row &w) const { return w.out_row; }
     __device__ float *record(const Piece &q) const {
@@ -223,12 +216,14 @@ struct TreePolicy {
     }
     __device__ float2 *record_ml(const Piece &q) const { return p.ws_ml + (size_t)q.slot * kRows * (PAIR + 1); }
 
-    // Warp 10: describes the segment that this share's beginning cuts first: the share
+    // Once, by warp 11: describes the segment that this share's beginning cuts first: the share
     // begins behind the segment's first tile and the share before it does not.  (An empty
     // share, of which there are some when the tiles are fewer than the CTAs, may do so.)
-    __device__ void side_warp(int lane) const {
-        if (lane != 0) return;
-        Cut cut = {-1, 0, 0, 0, cu[p.c.B], {0, 0, 0}};
+    bool described = false;
+    __device__ void side(int lane) {
+        if (lane != 0 || described) return;
+        described = true;
+        Cut cut = {-1, 0, 0, 0, cu[p.c.B], 0, {0, 0}};
         const int W = cut.W, c = blockIdx.x;
         if (u_begin > 0 && u_begin < W) {
             const int b = Iter(*this, false).b;
@@ -240,6 +235,7 @@ struct TreePolicy {
                 cut.b = b;
                 cut.g = seg / blocks;
                 cut.rb = seg % blocks;
+                cut.nd = s.y;
                 cut.last = (int)(((long long)(s0 + len) * p.C - 1) / W);
             }
         }
@@ -296,80 +292,60 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Merges the records of the segment cut at the start of share c = blockIdx.x:
-// M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  Threads are
-// record rows x SL slices of the records; columns [16 y, 16 y + 16) of d_h.
-// Reads are coalesced (column-major records).  Latency-bound: what the segment
-// is comes in one load, and a thread's records are asked for two at a time.
-template <int D, int PAIR, int SL>
-__global__ void __launch_bounds__(kRows *(PAIR + 1) * SL) decode_tree_combine(const TreeParams p) {
+// M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.  One thread per
+// record row, columns [8 y, 8 y + 8) of d_h; reads are coalesced (column-major
+// records).  Latency-bound: all that it needs of the segment comes in one load,
+// four records are asked for at a time, and the blocks fit the GPU at once.
+template <int D, int PAIR>
+__global__ void __launch_bounds__(kRows *(PAIR + 1)) decode_tree_combine(const TreeParams p) {
     constexpr int kRecRows = kRows * (PAIR + 1);
-    __shared__ float part[SL - 1][18][kRecRows];
-    const int t = threadIdx.x % kRecRows, slice = threadIdx.x / kRecRows;
+    const int t = threadIdx.x;
     const int hh = t >> 7, tok = (t & 127) / p.r, head = (t & 127) - tok * p.r;
-    const int col = blockIdx.y * 16;
+    const int col = blockIdx.y * 8;
     pdl_wait_primary();
-    const Cut cut = p.ws_cut[blockIdx.x];
-    if (cut.b < 0) return;
-    const int i = cut.rb * p.pb + hh * p.pt + tok;
-    const bool valid = tok < p.pt && i < seq_state(p, cut.b).y;
+    const int4 *desc = reinterpret_cast<const int4 *>(p.ws_cut + blockIdx.x);
+    const int4 d0 = desc[0], d1 = desc[1];
+    const int b = d0.x, g = d0.y, rb = d0.z, last = d0.w, W = d1.x, nd = d1.y;
+    const int i = rb * p.pb + hh * p.pt + tok;
+    if (b < 0 || tok >= p.pt || i >= nd) return;
     // the records: slot 2 c - 1 (the end of the share before), then slot 2 c of each share
     // up to the last that is not empty
-    const int first = blockIdx.x, n = cut.last - first + 2;
-    auto there = [&](int k) {
-        const int c = first + k - 1;
-        return k < n && (k == 0 || cut.W >= p.C || share_begin(c, cut.W, p.C) < share_begin(c + 1, cut.W, p.C));
-    };
-    float M = -INFINITY, L = 0.f, acc[16];
+    const int first = blockIdx.x, n = last - first + 2;
+    float M = -INFINITY, L = 0.f, acc[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-    auto slot = [&](int k) { return k == 0 ? 2 * (size_t)first - 1 : 2 * (size_t)(first + k - 1); };
-    auto add = [&](float2 v, const float (&o)[16]) {
-        const float Mn = fmaxf(M, v.x);
-        if (Mn == -INFINITY) return;  // nothing seen yet
-        const float a = fast_exp2(M - Mn), w = fast_exp2(v.x - Mn);
-        L = L * a + w * v.y;
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int k0 = 0; k0 < n; k0 += 4) {
+        float2 v[4];
+        float o[4][8];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[e] = acc[e] * a + w * o[e];
-        M = Mn;
-    };
-    if (valid)
-        for (int k = slice; k < n; k += 2 * SL) {
-            const bool one = there(k), two = there(k + SL);
-            if (!one && !two) continue;
-            const size_t s0 = slot(one ? k : k + SL), s1 = slot(two ? k + SL : k);
-            const float2 v0 = p.ws_ml[s0 * kRecRows + t], v1 = p.ws_ml[s1 * kRecRows + t];
-            const float *a = p.ws_o + (s0 * D + col) * kRecRows + t, *b = p.ws_o + (s1 * D + col) * kRecRows + t;
-            float o0[16], o1[16];
+        for (int j = 0; j < 4; ++j) {
+            const int k = k0 + j, c = first + k - 1;
+            v[j] = make_float2(-INFINITY, 0.f);
+            if (k >= n || (k > 0 && W < p.C && share_begin(c, W, p.C) == share_begin(c + 1, W, p.C))) continue;
+            const size_t slot = 2 * (size_t)c + (k == 0 ? 1 : 0);
+            v[j] = p.ws_ml[slot * kRecRows + t];
+            const float *src = p.ws_o + (slot * D + col) * kRecRows + t;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o0[e] = a[(size_t)e * kRecRows];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o1[e] = b[(size_t)e * kRecRows];
-            if (one) add(v0, o0);
-            if (two) add(v1, o1);
+            for (int e = 0; e < 8; ++e) o[j][e] = src[(size_t)e * kRecRows];
         }
-    if (slice > 0) {
-        part[slice - 1][16][t] = M;
-        part[slice - 1][17][t] = L;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) part[slice - 1][e][t] = acc[e];
-    }
-    __syncthreads();
-    if (slice > 0 || !valid) return;
+        for (int j = 0; j < 4; ++j) {
+            if (v[j].x == -INFINITY) continue;  // no record, or nothing seen yet
+            const float Mn = fmaxf(M, v[j].x);
+            const float a = fast_exp2(M - Mn), w = fast_exp2(v[j].x - Mn);
+            L = L * a + w * v[j].y;
 #pragma unroll
-    for (int s = 0; s < SL - 1; ++s) {
-        float o[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = part[s][e][t];
-        add(make_float2(part[s][16][t], part[s][17][t]), o);
+            for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + w * o[j][e];
+            M = Mn;
+        }
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    uint32_t pk[8];
+    uint32_t pk[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) pk[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    uint4 *d4 = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                          (((size_t)cut.b * p.n + i) * p.H + cut.g * p.r + head) * D + col);
-    d4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-    d4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+    for (int e = 0; e < 4; ++e) pk[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                               (((size_t)b * p.n + i) * p.H + g * p.r + head) * D + col) =
+        make_uint4(pk[0], pk[1], pk[2], pk[3]);
 }
 
 template <int D, int PAIR>
@@ -378,7 +354,6 @@ struct TreeTag {};
 template <int D, int PAIR>
 cudaError_t run_tree(const TreeParams &p, const CUtensorMap *tmq, const CUtensorMap *tmk, const CUtensorMap *tmv,
                      cudaStream_t st) {
-    constexpr int kSlices = PAIR ? 2 : 4;
     auto kern = decode_tree_kernel<D, PAIR>;
     cudaError_t e = once_per_device<TreeTag<D, PAIR>>([&] {
         cudaFuncAttributes fa;
@@ -390,8 +365,7 @@ cudaError_t run_tree(const TreeParams &p, const CUtensorMap *tmq, const CUtensor
     if (e != cudaSuccess) return e;
     e = dec::launch_pdl(kern, dim3(p.C), dim3(kThreads), tree_smem<D, PAIR>(p.c.B), st, *tmq, *tmk, *tmv, p);
     if (e != cudaSuccess) return e;
-    return dec::launch_pdl(decode_tree_combine<D, PAIR, kSlices>, dim3(p.C, D / 16),
-                           dim3(kRows * (PAIR + 1) * kSlices), 0, st, p);
+    return dec::launch_pdl(decode_tree_combine<D, PAIR>, dim3(p.C, D / 8), dim3(kRows * (PAIR + 1)), 0, st, p);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }

@@ -10,7 +10,7 @@
 // floor(128 / r) consecutive positions of one sequence, all r heads of one
 // group, against the key tiles that they see.
 //
-// Work list.  The lengths are on the device, so warp 10 of each CTA finds the
+// Work list.  The lengths are on the device, so warp 11 of each CTA finds the
 // CTA's pieces from cu as it goes and passes them to the other roles through a
 // ring in shared memory.  Pieces are ordered by their index x within the
 // sequence, the largest first, so that the ones with the most keys start first
@@ -29,7 +29,8 @@ namespace {
 
 using namespace att;
 
-constexpr int kRing = 8;  // pieces between the list's warp and the slowest role
+constexpr int kRing = 8;   // pieces between the list and the slowest role
+constexpr int kAhead = 3;  // entries filled ahead of warp 11's own
 
 struct PackedParams {
     const int32_t *cu;
@@ -72,8 +73,8 @@ struct PackedPolicy {
         return make_int2(a, min(max(p.cu[b + 1], a), p.N) - a);
     }
 
-    // The 11 consumers of a ring entry: the two TMA warps, the MMA thread, the softmax warps.
-    static constexpr int kConsumers = 11;
+    // The consumers of a ring entry: the two TMA warps, the two MMA threads, the softmax warps.
+    static constexpr int kConsumers = 12;
 
     struct Iter {
         PackedPolicy &pol;
@@ -135,81 +136,94 @@ struct PackedPolicy {
         w.out_row = ok ? (q.start + w.pos) * p.H + q.g * p.r + head : -1;
         return w;
     }
-    // whether some row of the warp's tile does not see all of key tile j
-    __device__ bool masked(const Piece &q, const Row &, int j) const {
-        const int key0 = (q.j_lo + j) * kKeys;
-        const int first = q.s0 + ((threadIdx.x >> 7) & 1) * p.pt;
+    __device__ bool masked(const Piece &q, int hh, int j) const {
+        const int key0 = (q.j_lo + j) * kKeys, first = q.s0 + hh * p.pt;
         return key0 + kKeys - 1 > first || (p.window > 0 && key0 < first + p.pt - p.window);
     }
-    __device__ void mask(const Piece &q, const Row &w, int j, uint32_t (&sr)[4][32]) const {
-        const int key0 = (q.j_lo + j) * kKeys;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int key = key0 + c * 32 + e;
-                if (key > w.pos || key < w.key_lo) sr[c][e] = __float_as_uint(-INFINITY);
-            }
+    __device__ uint32_t words(const Piece &q, const Row &w, int j, int c) const {
+        const int key0 = (q.j_lo + j) * kKeys + c * 32;
+        const int hi = w.pos - key0, lo = max(w.key_lo, 0) - key0;  // keys [lo, hi] of the chunk
+        uint32_t bits = hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1u;
+        if (lo > 0) bits &= lo > 31 ? 0u : 0xffffffffu << lo;
+        return bits;
     }
     __device__ int out_row(const Piece &, const Row &w) const { return w.out_row; }
     __device__ float *record(const Piece &) const { return nullptr; }
     __device__ float2 *record_ml(const Piece &) const { return nullptr; }
 
-    // Warp 10: fills the ring.
-    __device__ void side_warp(int lane) {
+    // The list's state, in warp 11.
+    struct List {
+        int i = 0;      // entries filled
+        int x, at;      // the level: pieces of index x; how many sequences (of one group) have one
+        int below = 0;  // pieces of the levels before
+        int b0 = 0, seen = 0;  // the level's scan: sequences before b0, `seen` of them in the level
+        bool begun = false, ended = false;
+    } list;
+
+    // Keeps the ring a few entries ahead of warp 11's own walk.  (Filling entry i waits
+    // until every role is through with entry i - kRing, which none of them needs this
+    // warp for: it has long loaded that piece.)
+    __device__ void side(int lane) {
         const int p2 = 2 * p.pt, B = p.B, C = gridDim.x;
-        int top = 0;
-        for (int b = lane; b < B; b += 32) top = max(top, counts[b]);
-        top = __reduce_max_sync(0xffffffffu, top);
         auto reach = [&](int x) {  // sequences with a piece of index x
             int n = 0;
             for (int b = lane; b < B; b += 32) n += counts[b] > x ? 1 : 0;
             return (int)__reduce_add_sync(0xffffffffu, n);
         };
-        int x = top - 1;                        // the level: pieces of index x
-        int at = x >= 0 ? reach(x) : 0;         // how many of them
-        long long below = 0;                    // pieces of the levels before
-        int b0 = 0, seen = 0;                   // the level's scan: sequences before b0, `seen` of them in it
-        for (int i = 0;; ++i) {
+        List &s = list;
+        if (!s.begun) {
+            int top = 0;
+            for (int b = lane; b < B; b += 32) top = max(top, counts[b]);
+            s.x = __reduce_max_sync(0xffffffffu, top) - 1;
+            s.at = s.x >= 0 ? reach(s.x) : 0;
+        }
+        const int until = s.begun ? s.i + 1 : kAhead;
+        s.begun = true;
+        for (; s.i < until && !s.ended; ++s.i) {
+            const int i = s.i;
             // the CTA's i-th piece: turns run forward and backward
-            const long long u = (long long)i * C + ((i & 1) ? C - 1 - (int)blockIdx.x : (int)blockIdx.x);
-            const long long v = u / p.G;
-            while (x >= 0 && v >= below + at) {
-                below += at;
-                --x;
-                at = x >= 0 ? reach(x) : 0;
-                b0 = seen = 0;
+            const int u = i * C + ((i & 1) ? C - 1 - (int)blockIdx.x : (int)blockIdx.x);
+            const int v = u / p.G;
+            while (s.x >= 0 && v >= s.below + s.at) {
+                s.below += s.at;
+                --s.x;
+                s.at = s.x >= 0 ? reach(s.x) : 0;
+                s.b0 = s.seen = 0;
             }
+            // the (v - below)-th sequence of the level: the lane that holds it writes the entry
             int4 e = make_int4(0, 0, 0, -1);
-            if (x >= 0) {
-                const int k = (int)(v - below);
-                for (;; b0 += 32) {  // (b0 < B: the level has more than k pieces)
-                    const int b = b0 + lane;
-                    const unsigned has = __ballot_sync(0xffffffffu, b < B && counts[b] > x);
-                    const int n = __popc(has);
-                    if (k < seen + n) {
-                        const int2 s = span(p, b0 + __fns(has, 0, k - seen + 1));
-                        e = make_int4(s.x, s.y, x * p2, (int)(u - v * p.G));
-                        break;
+            bool found = false;
+            while (s.x >= 0) {  // (ends: the level has more than v - below sequences)
+                const int b = s.b0 + lane;
+                const unsigned has = __ballot_sync(0xffffffffu, b < B && counts[b] > s.x);
+                const int n = __popc(has), k = v - s.below - s.seen;
+                if (k < n) {
+                    found = ((has >> lane) & 1u) && __popc(has & ((1u << lane) - 1u)) == k;
+                    if (found) {
+                        const int2 w = span(p, b);
+                        e = make_int4(w.x, w.y, s.x * p2, u - v * p.G);
                     }
-                    seen += n;
+                    break;
                 }
+                s.seen += n;
+                s.b0 += 32;
             }
+            s.ended = s.x < 0;
             const int slot = i % kRing;
             if (i >= kRing) {
                 const bool ok = *vabort == 0 && mbar_wait(&taken[slot], ((i / kRing) & 1) ^ 1, timeout_ns);
                 if (!__all_sync(0xffffffffu, ok)) {
                     if (lane == 0) set_status(status, STATUS_TIMEOUT);
                     *vabort = 1;
+                    s.ended = true;
                     return;
                 }
             }
-            if (lane == 0) {
+            if (found || (s.ended && lane == 0)) {
                 ring[slot] = e;
                 mbar_arrive(&filled[slot]);
             }
             __syncwarp();
-            if (e.w < 0) return;
         }
     }
 };
