@@ -502,11 +502,13 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
             // pieces.  Round k issues P.V of tile k - LOOK and S of tile k, where they are this
             // issuer's.  What the round needs is looked up and waited for before its wait for P:
             // from there to the S is on every tile's critical path.
-            // The issuers take turns, a group [P.V of one tile, S of the next] each.  Left to
-            // themselves they fall into step: both softmaxes then share the SM's issue slots, both
-            // groups the tensor core, and neither overlaps the other (4,800 cycles a tile of a pair
-            // against 3,990; passing the turn on before the S took 4,300, one thread for both row
-            // tiles 4,400).
+            // In pieces of kTurnTiles or more the issuers of a pair take turns, a group [P.V of one
+            // tile, S of the next] each.  Left to themselves they fall into step: both softmaxes
+            // then share the SM's issue slots, both groups the tensor core, and neither overlaps the
+            // other (4,800 cycles a tile against 3,990; passing the turn on before the S took 4,300,
+            // one thread for both row tiles 4,400).  In short pieces the order only costs (89 against
+            // 87 us for 96 short prompts).  With alternate key tiles each round is one issuer's.
+            constexpr int kTurnTiles = 4;
             constexpr int LOOK = PAIR ? 1 : 2;
             typename Pol::Iter sw(pol, false), vw(pol, false);
             Piece sq, vq;
@@ -536,7 +538,8 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
                 const bool act = PAIR || (k & 1) == hh;  // this issuer's round
                 if (s_ready && act && !wait(&bar.k_full[ks], (k / ST) & 1)) break;
                 if (mine && !wait(&bar.p_ready[hh], cnt++ & 1)) break;
-                if (act && (hh == 1 || turns > 0) && !wait(&bar.turn[hh], (turns - 1 + hh) & 1)) break;
+                const bool turn = PAIR ? pv && v_n >= kTurnTiles : act;  // the same for both
+                if (turn && (hh == 1 || turns > 0) && !wait(&bar.turn[hh], (turns - 1 + hh) & 1)) break;
                 if (mine) {
                     tc::fence_after();
                     const uint64_t d = dv + ((vs * kTile) >> 4);
@@ -560,7 +563,7 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
                 // turn is passed on, since it may have to wait.
                 const bool opens = !s_ready;
                 if (opens) {
-                    if (act) mbar_arrive(&bar.turn[hh ^ 1]);
+                    if (turn) mbar_arrive(&bar.turn[hh ^ 1]);
                     if (more) more = sw.next(sq);
                     if (more) {
                         ++s_piece;
@@ -589,7 +592,7 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
                     }
                     if (++s_j == s_n) tc::commit(&bar.q_empty[s_piece % NQ]);
                 }
-                if (act) {
+                if (turn) {
                     if (!opens) mbar_arrive(&bar.turn[hh ^ 1]);
                     ++turns;
                 }

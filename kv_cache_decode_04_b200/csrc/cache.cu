@@ -41,14 +41,16 @@ __device__ __forceinline__ size_t piece_of(const CacheView &c, int page, int g, 
 // ------------------------------------------------------------------ append
 
 constexpr int kAppendWarps = 8;
+constexpr int kAppendHeld = 4;  // pieces of K and of V that a lane has in flight
 
 // One warp per new token: it finds the token's sequence in cu_seqlens (a
 // binary search over B + 1 entries), then moves the token's G rows of K and of
-// V.  HBM-bound for prompts: each byte is read once and written once.
+// V, all loads of a round before its stores.  HBM-bound for prompts: each byte
+// is read once and written once.
 __global__ void __launch_bounds__(kAppendWarps * 32)
-    cache_append_kernel(const uint4 *k_new, const uint4 *v_new, const int32_t *cu, const int32_t *seqlens,
-                        int32_t *seqlens_out, uint4 *k_cache, uint4 *v_cache, const CacheView c, int N,
-                        unsigned *status) {
+    cache_append_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new, const int32_t *cu,
+                        const int32_t *seqlens, int32_t *seqlens_out, uint4 *__restrict__ k_cache,
+                        uint4 *__restrict__ v_cache, const CacheView c, int N, unsigned *status) {
     pdl_wait_primary();
     const int lane = threadIdx.x & 31;
     const int gid = blockIdx.x * blockDim.x + threadIdx.x;
@@ -60,6 +62,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
         seqlens_out[b] = ok ? T + (hi - lo) : T;
     }
     const int end = min(N, max(0, cu[c.B]));
+    const int pieces = c.G * c.row16;
+    const int shift = __ffs(c.row16) - 1;  // pieces of a row: 8, 16 or 32
     for (int tok = gid >> 5; tok < end; tok += (gridDim.x * blockDim.x) >> 5) {
         int lo = 0, hi = c.B - 1;  // the last b with cu[b] <= tok
         while (lo < hi) {
@@ -76,12 +80,26 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
             if (lane == 0) set_status(status, STATUS_PAGES);
             continue;
         }
-        const size_t src = (size_t)tok * c.G * c.row16;
-        for (int i = lane; i < c.G * c.row16; i += 32) {
-            const int g = i / c.row16, e = i - g * c.row16;
-            const size_t dst = piece_of(c, page, g, row) + e;
-            k_cache[dst] = k_new[src + i];
-            v_cache[dst] = v_new[src + i];
+        const size_t src = (size_t)tok * pieces;
+        for (int i0 = lane; i0 < pieces; i0 += 32 * kAppendHeld) {
+            uint4 k[kAppendHeld], v[kAppendHeld];
+#pragma unroll
+            for (int j = 0; j < kAppendHeld; ++j) {
+                const int i = i0 + j * 32;
+                if (i < pieces) {
+                    k[j] = __ldcs(k_new + src + i);
+                    v[j] = __ldcs(v_new + src + i);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kAppendHeld; ++j) {
+                const int i = i0 + j * 32;
+                if (i < pieces) {
+                    const size_t dst = piece_of(c, page, i >> shift, row) + (i & (c.row16 - 1));
+                    k_cache[dst] = k[j];
+                    v_cache[dst] = v[j];
+                }
+            }
         }
     }
 }
@@ -90,27 +108,30 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
 
 constexpr int kCompactThreads = 256;
 constexpr int kKeepMax = 64;
-constexpr int kHeld = kKeepMax * 32 / kCompactThreads;  // 16-byte pieces a thread holds (fp32 d_h 128: 32 a row)
 
 // One block per (sequence, KV head, K or V).  All kept rows are read into
 // registers before any is written, so any order of `keep`, repeated entries
-// included, gives the rows as they were before the call.
+// included, gives the rows as they were before the call.  Latency-bound: three
+// dependent loads (lengths and entries, pages, rows), so the registers are kept
+// few (ROW16 16-byte pieces a row) and eight blocks share an SM.
+template <int ROW16>
 __global__ void __launch_bounds__(kCompactThreads)
     cache_compact_kernel(uint4 *k_cache, uint4 *v_cache, const int32_t *seqlens, const int32_t *keep,
                          const int32_t *n_keep, int32_t *seqlens_out, const CacheView c, int m, unsigned *status) {
+    constexpr int kHeld = kKeepMax * ROW16 / kCompactThreads;  // pieces a thread holds
     __shared__ size_t src[kKeepMax], dst[kKeepMax];
     __shared__ int moves[kKeepMax];
     pdl_wait_primary();
     const int b = blockIdx.x / (2 * c.G), rem = blockIdx.x % (2 * c.G);
     const int g = rem >> 1;
     uint4 *cache = (rem & 1) ? v_cache : k_cache;
+    const int j = threadIdx.x;
+    const int from = j < m ? keep[(size_t)b * m + j] : 0;
     const int T = seqlens[b];
     const int n = n_keep ? n_keep[b] : m;
     bool ok = T >= 0 && T <= c.cap && n >= 0 && n <= m;
     bool paged = true;
-    const int j = threadIdx.x;
     if (ok && j < n) {
-        const int from = keep[(size_t)b * m + j];
         ok = from >= 0 && from < kKeepMax && T <= c.cap - 1 - max(from, j);
         if (ok) {
             int p0, r0, p1, r1;
@@ -132,23 +153,17 @@ __global__ void __launch_bounds__(kCompactThreads)
     }
     if (!go) return;
     uint4 held[kHeld];
-    const int pieces = n * c.row16;
+    const int pieces = n * ROW16;
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
         const int p = i * kCompactThreads + threadIdx.x;
-        if (p < pieces) {
-            const int row = p / c.row16;
-            if (moves[row]) held[i] = cache[src[row] + (p - row * c.row16)];
-        }
+        if (p < pieces && moves[p / ROW16]) held[i] = cache[src[p / ROW16] + p % ROW16];
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
         const int p = i * kCompactThreads + threadIdx.x;
-        if (p < pieces) {
-            const int row = p / c.row16;
-            if (moves[row]) cache[dst[row] + (p - row * c.row16)] = held[i];
-        }
+        if (p < pieces && moves[p / ROW16]) cache[dst[p / ROW16] + p % ROW16] = held[i];
     }
 }
 
@@ -406,9 +421,15 @@ cudaError_t launch_cache_append(const void *k_new, const void *v_new, const int3
 cudaError_t launch_cache_compact(void *k_cache, void *v_cache, const int32_t *seqlens, const int32_t *keep,
                                  const int32_t *n_keep, int32_t *seqlens_out, const CacheView &c, int m,
                                  unsigned *status, cudaStream_t st) {
-    return dec::launch_pdl(cache_compact_kernel, dim3(c.B * c.G * 2), dim3(kCompactThreads), 0, st,
-                           static_cast<uint4 *>(k_cache), static_cast<uint4 *>(v_cache), seqlens, keep, n_keep,
-                           seqlens_out, c, m, status);
+    auto launch = [&](auto kern) {
+        return dec::launch_pdl(kern, dim3(c.B * c.G * 2), dim3(kCompactThreads), 0, st, static_cast<uint4 *>(k_cache),
+                               static_cast<uint4 *>(v_cache), seqlens, keep, n_keep, seqlens_out, c, m, status);
+    };
+    switch (c.row16) {  // d_h 64 or 128, bf16 or fp32
+    case 8: return launch(cache_compact_kernel<8>);
+    case 16: return launch(cache_compact_kernel<16>);
+    default: return launch(cache_compact_kernel<32>);
+    }
 }
 
 cudaError_t launch_pages_release(int32_t *table, int32_t *refcount, const int32_t *lengths, int B, int M, int page,
