@@ -392,14 +392,17 @@ def layer_decode_step(h, W_Q, W_K, W_V, W_O, k_cache, v_cache, seqlens, scale=No
 # builds an object around it in 3 us).
 
 
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def _ready(names, *tensors):
     """Every tensor (None: absent) is contiguous and on the current CUDA device, whose index it returns."""
     index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+        if t is not None and not (t.get_device() == index and t.is_contiguous()):
             break
     else:
-        if index >= 0 and torch._C._cuda_getDevice() == index:
+        if index >= 0 and _current_device() == index:
             return index
     for name, t in zip(names.split(), tensors):
         if t is None:
@@ -414,15 +417,18 @@ def _ready(names, *tensors):
 
 
 def _handle(stream, index):
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return _current_stream(index) if stream is None else stream.cuda_stream
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_I32 = torch.int32
+
+
 def _int32(name, t, *shape):
-    if t.dtype != torch.int32 or t.shape != shape:
+    if t.dtype is not _I32 or t.shape != shape:
         raise ValueError("%s must be int32 %s" % (name, list(shape)))
 
 
@@ -437,17 +443,21 @@ def _empty(stream, like, size=None, dtype=None):
 
 
 def _cache(k_cache, v_cache, block_table, B):
-    """(table pointer, G, page, num_pages, M) of a paged cache, or of a dense one without a table."""
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+    """(table pointer, G, page, num_pages, M, d_h, dtype code) of a paged cache, or of a dense one
+    without a table."""
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not dtype:
         raise ValueError("k_cache and v_cache must share a 4-d shape and a dtype")
-    P, G, page, _ = k_cache.shape
+    P, G, page, d_h = shape
+    code = _dtype_code(k_cache)
     if block_table is None:
         if P != B:
             raise ValueError("a dense cache must be [B, G, T_cap, d_h] with B = %d" % B)
-        return None, G, page, P, 1
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
+        return None, G, page, P, 1, d_h, code
+    rows = block_table.shape
+    if block_table.dtype is not _I32 or len(rows) != 2 or rows[0] != B:
         raise ValueError("block_table must be int32 [B, M] with B = %d" % B)
-    return block_table.data_ptr(), G, page, P, block_table.shape[1]
+    return block_table.data_ptr(), G, page, P, rows[1], d_h, code
 
 
 def prefill_packed(q, k, v, cu_seqlens, scale=None, out=None, stream=None, window=0):
@@ -500,12 +510,11 @@ def decode_tree(q, k_cache, v_cache, seqlens, tree_mask=None, n_draft=None, bloc
     are left as they were.
     """
     B, n, H, d_h = q.shape
-    table, G, page, P, M = _cache(k_cache, v_cache, block_table, B)
-    if k_cache.shape[3] != d_h:
+    table, G, page, P, M, d_c, code = _cache(k_cache, v_cache, block_table, B)
+    if d_c != d_h:
         raise ValueError("q and the caches disagree on d_h")
-    if q.dtype != k_cache.dtype:
+    if q.dtype is not k_cache.dtype:
         raise TypeError("q, k_cache and v_cache must share a dtype")
-    code = _dtype_code(q)
     _int32("seqlens", seqlens, B)
     if tree_mask is not None and (tree_mask.dtype != torch.int64 or tree_mask.shape != (B, n)):
         raise ValueError("tree_mask must be int64 [B, n]")
@@ -536,14 +545,13 @@ def cache_append(k_new, v_new, cu_seqlens, seqlens, k_cache, v_cache, block_tabl
     Returns seqlens_out [B] = seqlens + the rows of each.  block_table None: dense caches.
     """
     B = seqlens.numel()
-    table, G, page, P, M = _cache(k_cache, v_cache, block_table, B)
-    d_h = k_cache.shape[3]
-    N = k_new.shape[0]
-    if k_new.shape != (N, G, d_h) or v_new.shape != k_new.shape:
+    table, G, page, P, M, d_h, code = _cache(k_cache, v_cache, block_table, B)
+    rows, dtype = k_new.shape, k_cache.dtype
+    N = rows[0]
+    if rows != (N, G, d_h) or v_new.shape != rows:
         raise ValueError("k_new and v_new must be [N, G, d_h] of the caches' G and d_h")
-    if k_new.dtype != k_cache.dtype or v_new.dtype != k_cache.dtype:
+    if k_new.dtype is not dtype or v_new.dtype is not dtype:
         raise TypeError("the new rows and the caches must share a dtype")
-    code = _dtype_code(k_cache)
     _int32("seqlens", seqlens, B)
     _int32("cu_seqlens", cu_seqlens, B + 1)
     if seqlens_out is None:
@@ -565,8 +573,7 @@ def cache_compact(k_cache, v_cache, seqlens, keep, n_keep=None, block_table=None
     Returns seqlens_out [B] = seqlens + n_keep.  block_table None: dense caches.
     """
     B = seqlens.numel()
-    table, G, page, P, M = _cache(k_cache, v_cache, block_table, B)
-    code = _dtype_code(k_cache)
+    table, G, page, P, M, d_h, code = _cache(k_cache, v_cache, block_table, B)
     _int32("seqlens", seqlens, B)
     m = keep.shape[1] if keep.dim() == 2 else 0
     _int32("keep", keep, B, m)
@@ -579,17 +586,18 @@ def cache_compact(k_cache, v_cache, seqlens, keep, n_keep=None, block_table=None
     index = _ready("k_cache v_cache seqlens keep n_keep seqlens_out block_table", k_cache, v_cache, seqlens, keep,
                    n_keep, seqlens_out, block_table)
     _check(lib.gqa_cache_compact(k_cache.data_ptr(), v_cache.data_ptr(), table, seqlens.data_ptr(), keep.data_ptr(),
-                                 _ptr(n_keep), seqlens_out.data_ptr(), B, m, G, k_cache.shape[3], page, P, M, code,
+                                 _ptr(n_keep), seqlens_out.data_ptr(), B, m, G, d_h, page, P, M, code,
                                  _handle(stream, index)))
     return seqlens_out
 
 
 def _pool(block_table, refcount):
-    if block_table.dtype != torch.int32 or block_table.dim() != 2:
+    rows, counts = block_table.shape, refcount.shape
+    if block_table.dtype is not _I32 or len(rows) != 2:
         raise ValueError("block_table must be int32 [B, M]")
-    if refcount.dtype != torch.int32 or refcount.dim() != 1:
+    if refcount.dtype is not _I32 or len(counts) != 1:
         raise ValueError("refcount must be int32 [P]")
-    return block_table.shape[0], block_table.shape[1], refcount.shape[0]
+    return rows[0], rows[1], counts[0]
 
 
 @functools.lru_cache(maxsize=256)
@@ -601,11 +609,10 @@ def pages_reserve(block_table, refcount, seqlens, n_new, k_pages, v_pages, works
     """Makes positions [seqlens[b], seqlens[b] + n_new[b]) of every sequence its own: missing pages are
     taken from the pool (lowest free page first, in table order), shared ones are replaced by a copy.
     block_table [B,M] and refcount [P] int32 are updated in place.  All or nothing."""
-    B, M, P = _pool(block_table, refcount)
-    _, G, page, _, _ = _cache(k_pages, v_pages, block_table, B)
-    if k_pages.shape[0] != P:
-        raise ValueError("refcount must hold one count per page (%d)" % k_pages.shape[0])
-    code = _dtype_code(k_pages)
+    B, _, P = _pool(block_table, refcount)
+    table, G, page, pages, M, d_h, code = _cache(k_pages, v_pages, block_table, B)
+    if pages != P:
+        raise ValueError("refcount must hold one count per page (%d)" % pages)
     _int32("seqlens", seqlens, B)
     _int32("n_new", n_new, B)
     index = _ready("k_pages v_pages block_table refcount seqlens n_new workspace", k_pages, v_pages, block_table,
@@ -615,8 +622,8 @@ def pages_reserve(block_table, refcount, seqlens, n_new, k_pages, v_pages, works
         workspace = _empty(stream, k_pages, size, torch.uint8)
     else:
         size = workspace.numel() * workspace.element_size()
-    _check(lib.gqa_pages_reserve(block_table.data_ptr(), refcount.data_ptr(), seqlens.data_ptr(), n_new.data_ptr(),
-                                 k_pages.data_ptr(), v_pages.data_ptr(), B, G, k_pages.shape[3], page, P, M, code,
+    _check(lib.gqa_pages_reserve(table, refcount.data_ptr(), seqlens.data_ptr(), n_new.data_ptr(),
+                                 k_pages.data_ptr(), v_pages.data_ptr(), B, G, d_h, page, P, M, code,
                                  workspace.data_ptr(), size, _handle(stream, index)))
 
 

@@ -325,7 +325,6 @@ struct PieceBase {
     // keys of row tile 0 and 1, from the first key of the piece's first tile on (0:
     // the tile has no rows).  Row tile i visits ceil(k_i / 128) tiles.
     int k0, k1;
-    int v_end;   // keys from there on that belong to the sequence: V rows past them are cleared
     bool split;  // carry P as two bf16 terms
     __device__ int tiles() const { return (max(k0, k1) + kKeys - 1) / kKeys; }
 };
@@ -403,10 +402,11 @@ struct Barriers {
 //   pol.kv_look(piece, tile, lane)  what kv() needs from memory, asked for before the stage is free
 //   pol.q(piece, row tile, address, barrier)  loads of Q rows, by one lane; pol.q_bytes() each
 //   pol.masked(piece, row tile, tile)  whether some row does not see all of a key tile
-//   pol.row(piece, row tile, row)  -> Pol::Row, the thread's row
+//   pol.row(piece, row tile, row)  -> Pol::Row, the thread's row; its out_row: row of `out`, or -1
 //   pol.words(piece, row, tile, c)  what the row sees of the 32 keys of chunk c, as bits
+//   pol.clear_from(piece, row, tile), pol.clears(piece, row, tile, key)  V rows of the tile that
+//                                 nobody sees: the first that may be one (128: none), and which are
 //   pol.side(lane)                called by warp 11 before each of its pieces
-//   pol.out_row(piece, row)       row of `out`, or -1
 //   pol.record(piece)             null, or where this piece's partial results go (D x rows floats,
 //                                 column-major), and pol.record_ml(piece)
 template <int D, int PAIR, typename Pol>
@@ -626,7 +626,7 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
             return warp_wait(bar.meet, met++ & 1, limit);
         };
         // Writes a piece's output, or its partial record; sets ok when a wait runs out.
-        auto epilogue = [&](const Piece &now, const typename Pol::Row &mine, float m, float l) {
+        auto epilogue = [&](const Piece &now, int out_row, float m, float l) {
             const int keys = PAIR && hh ? now.k1 : now.k0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -659,7 +659,6 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
                 c0 = hh * NC;
             }
             if (!PAIR || keys > 0) {
-                const int out_row = pol.out_row(now, mine);
                 if (!rec) {
                     const float inv = L > 0.f ? 1.f / L : 0.f;
                     w0 *= inv;
@@ -708,14 +707,15 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
             }
         };
         Piece q, now;
-        typename Pol::Row row = {}, mine = {};
+        typename Pol::Row row = {};
+        int out_row = -1;
         float m = -INFINITY, l = 0.f;
         bool open = false;  // `now` waits for its epilogue
         while (ok) {
             // the next piece and its row are looked up while the last P.V of the one before runs
             const bool have = walk.next(q);
             if (have) row = pol.row(q, PAIR ? hh : 0, t);
-            if (open) epilogue(now, mine, m, l);
+            if (open) epilogue(now, out_row, m, l);
             open = have && ok;
             if (!open) break;
             const int n = q.tiles(), keys = PAIR && hh ? q.k1 : q.k0;
@@ -739,10 +739,11 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
                 } else {
                     softmax_part<D>(tS, tO, pol.scale_log2, first, q.split, nch, m, l,
                                     [&](int c) { return pol.words(q, row, j, c); });
-                    // V rows past the sequence's end: P is 0 there, but 0 times what they hold must
-                    // stay 0.  Each warpgroup clears those that its P.V reads, ahead of it (both may
-                    // write zeros over zeros); the stage cannot be refilled before that P.V.
-                    const int r0 = q.v_end - j * kKeys, r1 = 32 * nch;
+                    // V rows that no row of the piece sees, those past the sequence's end among them:
+                    // P is 0 there, but 0 times what they hold must stay 0.  Each warpgroup clears
+                    // those that its P.V reads, ahead of it (both may write zeros over zeros); the
+                    // stage cannot be refilled before that P.V.
+                    const int r0 = pol.clear_from(q, row, j), r1 = 32 * nch;
                     if (r0 < r1) {
                         if (!warp_wait(&bar.v_full[it % ST], (it / ST) & 1, limit)) {
                             ok = false;
@@ -751,6 +752,7 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
                         uint8_t *tile = sm + Lay::OFF_V + (it % ST) * kTile;
                         for (int i = t; i < (r1 - r0) * HALVES * 8; i += 128) {
                             const int rr = r0 + i / (HALVES * 8), rem = i % (HALVES * 8);
+                            if (!pol.clears(q, row, j, rr)) continue;
                             asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
                                              smem_u32(tile + (rem >> 3) * kHalf + rr * 128 + (rem & 7) * 16)),
                                          "r"(0u)
@@ -764,7 +766,7 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
                 mbar_arrive(&bar.p_ready[hh]);
             }
             now = q;
-            mine = row;
+            out_row = row.out_row;
         }
         if (!ok && lane == 0) {
             set_status(pol.status, STATUS_TIMEOUT);

@@ -116,6 +116,7 @@ struct TreePolicy {
     };
     struct Row {
         uint64_t bits;  // drafts that the row sees
+        uint64_t seen;  // drafts that some row of the row block sees
         int out_row;
     };
 
@@ -152,7 +153,6 @@ struct TreePolicy {
                 const int keys = min(n_tok, j1 * kKeys) - j0 * kKeys;
                 q.k0 = keys;
                 q.k1 = PAIR && s.y - q.rb * p.pb > p.pt ? keys : 0;
-                q.v_end = n_tok - j0 * kKeys;
                 // as in the dense decode: P as two terms for at most 256 positions
                 q.split = n_tok <= 256;
                 return true;
@@ -198,7 +198,16 @@ struct TreePolicy {
     __device__ Row row(const Piece &q, int hh, int t) const {
         const int tok = t / p.r, head = t - tok * p.r;
         const int i = q.rb * p.pb + hh * p.pt + tok;  // draft
-        Row w = {0, -1};
+        Row w = {0, 0, -1};
+        const int d0 = q.rb * p.pb, d1 = min(q.nd, d0 + p.pb);  // the row block's drafts
+        if (p.mask) {
+            for (int k = d0 + (t & 31); k < d1; k += 32) w.seen |= (uint64_t)p.mask[(size_t)q.b * p.n + k];
+            w.seen = (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)w.seen) |
+                     (uint64_t)__reduce_or_sync(0xffffffffu, (uint32_t)(w.seen >> 32)) << 32;
+        } else {
+            w.seen = ~0ull >> (64 - d1);
+        }
+        w.seen &= ~0ull >> (64 - q.nd);
         if (tok < p.pt && i < q.nd && index_ok(q.b < p.c.B && i < p.n && q.g * p.r + head < p.H, status)) {
             w.bits = p.mask ? (uint64_t)p.mask[(size_t)q.b * p.n + i] : ~0ull >> (63 - i);
             w.bits &= ~0ull >> (64 - q.nd);
@@ -210,7 +219,16 @@ struct TreePolicy {
     __device__ uint32_t words(const Piece &q, const Row &w, int j, int c) const {
         return visible_word(w.bits, (q.j0 + j) * kKeys + c * 32 - q.T);
     }
-    __device__ int out_row(const Piece &, const Row &w) const { return w.out_row; }
+    // From the first draft on when there is one that nobody sees (a padded place that was never
+    // written, say), else from the sequence's end on.
+    __device__ int clear_from(const Piece &q, const Row &w, int j) const {
+        const bool gap = w.seen != (~0ull >> (64 - q.nd));
+        return max(0, q.T + (gap ? 0 : q.nd) - (q.j0 + j) * kKeys);
+    }
+    __device__ bool clears(const Piece &q, const Row &w, int j, int r) const {
+        const int rel = (q.j0 + j) * kKeys + r - q.T;
+        return rel >= 64 || !((w.seen >> rel) & 1u);
+    }
     __device__ float *record(const Piece &q) const {
         return q.slot < 0 ? nullptr : p.ws_o + (size_t)q.slot * D * kRows * (PAIR + 1);
     }

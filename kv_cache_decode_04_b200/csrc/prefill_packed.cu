@@ -103,7 +103,6 @@ struct PackedPolicy {
             const int base = q.j_lo * kKeys;
             q.k0 = min(q.len, q.s0 + p.pt) - base;
             q.k1 = q.s0 + p.pt < q.len ? min(q.len, q.s0 + 2 * p.pt) - base : 0;
-            q.v_end = q.len - base;
             q.split = base + max(q.k0, q.k1) <= kKeys || (p.window > 0 && p.window <= 256);
             return true;
         }
@@ -147,7 +146,9 @@ struct PackedPolicy {
         if (lo > 0) bits &= lo > 31 ? 0u : 0xffffffffu << lo;
         return bits;
     }
-    __device__ int out_row(const Piece &, const Row &w) const { return w.out_row; }
+    // keys past the sequence's end
+    __device__ int clear_from(const Piece &q, const Row &, int j) const { return q.len - (q.j_lo + j) * kKeys; }
+    __device__ bool clears(const Piece &, const Row &, int, int) const { return true; }
     __device__ float *record(const Piece &) const { return nullptr; }
     __device__ float2 *record_ml(const Piece &) const { return nullptr; }
 

@@ -102,6 +102,18 @@ def test_many_sequences_match_the_dense_call_and_themselves(gqa):
         ref.check(dense, r[a:z], w[a:z])
 
 
+def test_the_largest_batch(gqa):
+    """8192 sequences, every third empty."""
+    lens = [0 if b % 3 == 0 else b % 7 + 1 for b in range(8192)]
+    cu = offsets(lens)
+    q, k, v = inputs(cu, 2, 1, 64, seed=12)
+    got = run(gqa, q, k, v, cu)
+    for b in (0, 1, 2, 4000, 4001, 8189, 8190, 8191):
+        a, z = cu[b], cu[b + 1]
+        r, w = ref.prefill_packed(q[a:z], k[a:z], v[a:z], [0, z - a], 64 ** -0.5)
+        ref.check(got[a:z], r, w)
+
+
 def test_long_sequences_sampled(gqa):
     """3000 + 5000 + 1 tokens: rows across all key tiles."""
     cu = offsets([3001, 1, 5000])

@@ -110,6 +110,46 @@ def test_rows_that_see_nothing_are_zero(gqa):
     assert (got[0, 1] == 0).all() and (got[0, 2] == 0).all()
 
 
+@pytest.mark.parametrize("n,H,G,T", [(8, 4, 2, 100), (40, 8, 1, 115), (64, 8, 1, 0), (33, 2, 2, 127)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_drafts_that_no_mask_names_may_hold_anything(gqa, n, H, G, T, value):
+    """Padded places of a tree whose K/V were never written."""
+    x = Case(2, n, H, G, 64, 16, [T, 300], seed=n + T)
+    for b, gone in enumerate(([1, n - 1], [n // 2])):
+        clear = ~sum(1 << j for j in gone)
+        for i in range(n):
+            m = int(x.mask[b, i]) & clear & ((1 << 64) - 1)
+            x.mask[b, i] = m - (1 << 64) if m >= 1 << 63 else m
+        for j in gone:
+            p, r = ref.place(x.table, 16, b, x.seqlens[b] + j)
+            x.k[p, :, r] = value
+            x.v[p, :, r] = value
+    got = run(gqa, x)
+    for b, gone in enumerate(([1, n - 1], [n // 2])):
+        for j in gone:
+            p, r = ref.place(x.table, 16, b, x.seqlens[b] + j)
+            x.k[p, :, r] = 0  # (the definition's own 0 * NaN)
+            x.v[p, :, r] = 0
+    compare(got, x)
+
+
+def test_no_drafts_at_all_and_the_largest_batch(gqa):
+    x = Case(3, 2, 4, 2, 64, 16, [5, 0, 70], counts=[0, 0, 0], seed=31)
+    compare(run(gqa, x), x)
+    B = 8000
+    q = torch.randn((B, 1, 2, 64), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    k, v = (torch.randn((B, 1, 5, 64), generator=torch.Generator().manual_seed(s)).to(torch.bfloat16).cuda()
+            for s in (2, 3))
+    lens = [b % 5 for b in range(B)]
+    got = gqa.decode_tree(q, k, v, torch.tensor(lens, dtype=torch.int32).cuda()).cpu()
+    gqa.get_status()
+    for b in (0, 1, 4, 3999, 7998, 7999):
+        for h in range(2):
+            r, w = ref.attend(q[b, :, h].cpu(), k[b, 0, :lens[b] + 1].cpu(), v[b, 0, :lens[b] + 1].cpu(),
+                              torch.ones(1, lens[b] + 1, dtype=torch.bool), 64 ** -0.5)
+            ref.check(got[b, :, h], r, w)
+
+
 def test_one_draft_is_a_decode_step(gqa):
     """A single token over a dense cache: what gqa_decode gives over the lengths with that token."""
     x = Case(3, 1, 8, 2, 128, 0, [700, 1, 64], seed=14)
