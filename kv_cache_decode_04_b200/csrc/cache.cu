@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kPageThreads)
 // ------------------------------------------------------------------ reserve
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanLanes = 8;    // lanes that share a sequence
+constexpr int kPlanLanes = 4;    // lanes that share a sequence
 constexpr int kScanInts = 16;    // refcounts a thread looks at per step of the free-page scan
 
 // Exclusive sum over the block; `total` gets the whole sum.  Every thread calls it.
@@ -287,18 +287,19 @@ __device__ __forceinline__ void span(int T, int n, int page, int M, int &lo, int
     }
 }
 
-// Whether entry e has to get a page: it has none, or it shares one.  An entry
-// out of range, or of a page that nobody holds, counts as a missing one (and is
-// flagged where it is first seen).
-__device__ __forceinline__ bool takes_page(int e, const int32_t *refcount, int P) {
-    return e < 0 || e >= P || refcount[e] != 1;
-}
-
+// An entry has to get a page (in the plan below: held != 1) when it has none,
+// when it shares one, and when it is out of range or names a page that nobody
+// holds, which is flagged.
 // The plan, one block: which entries take a page (decided on the reference
 // counts before the call), the lowest free pages for them in table order, the
 // new table and counts, and per sequence the copy that the second kernel makes.
 // All or nothing: with too few free pages nothing changes.
 // ws: free pages [P], references to drop [P], jobs [B] (int4).
+// Latency-bound: a chain of dependent loads (lengths, entries, counts) and the
+// scan.  Each group of lanes keeps what it read of its first sequence's first
+// entries, so that up to 256 sequences of a few entries are read once (256 rows
+// over 15,000 pages: 7.5 us; read again in step 4, with eight lanes a sequence,
+// 12.8 us).
 __global__ void __launch_bounds__(kPlanThreads)
     pages_reserve_plan(int32_t *table, int32_t *refcount, const int32_t *seqlens, const int32_t *n_new, int B, int M,
                        int page, int P, int32_t *ws_free, int32_t *ws_drop, int4 *ws_job, unsigned *status) {
@@ -308,17 +309,30 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int tid = threadIdx.x;
     const int sub = tid & (kPlanLanes - 1), group = tid / kPlanLanes;
     constexpr int kGroups = kPlanThreads / kPlanLanes;
-    const unsigned gmask = ((1u << kPlanLanes) - 1) << ((tid & 31) & ~(kPlanLanes - 1));
+    const int base_lane = (tid & 31) & ~(kPlanLanes - 1);
+    const unsigned gmask = ((1u << kPlanLanes) - 1) << base_lane;
+    // this lane's first entry of the group's first sequence
+    int T0 = 0, n0 = 0, e0 = -1, r0 = 0;
     // 1. how many pages each sequence takes
     for (int b = group; b < B; b += kGroups) {
         int lo, hi, count = 0;
         bool ok;
-        span(seqlens[b], n_new[b], page, M, lo, hi, ok);
+        const int T = seqlens[b], n = n_new[b];
+        span(T, n, page, M, lo, hi, ok);
         if (!ok && sub == 0) set_status(status, STATUS_SEQLEN);
         for (int k = lo + sub; k < hi; k += kPlanLanes) {
             const int e = table[(size_t)b * M + k];
-            if (e >= P || (e >= 0 && refcount[e] < 1)) set_status(status, STATUS_PAGES);
-            count += takes_page(e, refcount, P) ? 1 : 0;
+            const int held = e >= 0 && e < P ? refcount[e] : 0;
+            if (e >= P || (e >= 0 && held < 1)) set_status(status, STATUS_PAGES);
+            count += held != 1 ? 1 : 0;
+            if (k == lo + sub && b == group) {
+                e0 = e;
+                r0 = held;
+            }
+        }
+        if (b == group) {
+            T0 = T;
+            n0 = n;
         }
 #pragma unroll
         for (int o = kPlanLanes / 2; o > 0; o >>= 1) count += __shfl_xor_sync(gmask, count, o);
@@ -338,12 +352,21 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     // 3. the `total` lowest free pages
     int found = 0;
+    const bool wide = (reinterpret_cast<uintptr_t>(refcount) & 15) == 0;
     for (int base = 0; base < P && found < total; base += kPlanThreads * kScanInts) {
         const int p0 = base + tid * kScanInts;
         unsigned bits = 0;
+        if (wide && p0 + kScanInts <= P) {
 #pragma unroll
-        for (int i = 0; i < kScanInts; ++i)
-            if (p0 + i < P && refcount[p0 + i] == 0) bits |= 1u << i;
+            for (int i = 0; i < kScanInts / 4; ++i) {
+                const int4 v = *reinterpret_cast<const int4 *>(refcount + p0 + 4 * i);
+                bits |= ((v.x == 0 ? 1u : 0u) | (v.y == 0 ? 2u : 0u) | (v.z == 0 ? 4u : 0u) | (v.w == 0 ? 8u : 0u))
+                        << (4 * i);
+            }
+        } else {
+            for (int i = 0; i < kScanInts; ++i)
+                if (p0 + i < P && refcount[p0 + i] == 0) bits |= 1u << i;
+        }
         int here;
         int at = found + block_scan(__popc(bits), sums, here);
         for (; bits && at < total; bits &= bits - 1) ws_free[at++] = p0 + __ffs(bits) - 1;
@@ -357,22 +380,29 @@ __global__ void __launch_bounds__(kPlanThreads)
     for (int b = group; b < B; b += kGroups) {
         int lo, hi;
         bool ok;
-        const int T = seqlens[b];
-        span(T, n_new[b], page, M, lo, hi, ok);
+        const bool first = b == group;
+        const int T = first ? T0 : seqlens[b];
+        span(T, first ? n0 : n_new[b], page, M, lo, hi, ok);
         int at = need[b];
         int4 job = make_int4(0, 0, 0, 0);
         for (int k0 = lo; k0 < hi && enough; k0 += kPlanLanes) {
             const int k = k0 + sub;
-            const int e = k < hi ? table[(size_t)b * M + k] : -1;
-            const bool take = k < hi && takes_page(e, refcount, P);
-            const unsigned votes = (__ballot_sync(gmask, take) & gmask) >> ((tid & 31) & ~(kPlanLanes - 1));
+            int e = -1, held = 1;
+            if (first && k0 == lo) {
+                e = e0;
+                held = k < hi ? r0 : 1;
+            } else if (k < hi) {
+                e = table[(size_t)b * M + k];
+                held = e >= 0 && e < P ? refcount[e] : 0;
+            }
+            const bool take = held != 1;
+            const unsigned votes = (__ballot_sync(gmask, take) & gmask) >> base_lane;
             if (take) {
                 const int slot = at + __popc(votes & ((1u << sub) - 1));
                 const int fresh = ws_free[slot];
-                const bool had = e >= 0 && e < P && refcount[e] > 1;
-                ws_drop[slot] = had ? e : -1;
+                ws_drop[slot] = held > 1 ? e : -1;
                 table[(size_t)b * M + k] = fresh;
-                if (had && k == lo) job = make_int4(e, fresh, T - lo * page, 0);
+                if (held > 1 && k == lo) job = make_int4(e, fresh, T - lo * page, 0);
             }
             at += __popc(votes);
         }
