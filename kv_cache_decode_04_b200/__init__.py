@@ -1,10 +1,11 @@
 """Grouped-query attention (GQA) on NVIDIA B200: Python binding of libgqa.so.
 
 Argument marshalling only: every step of the computation runs in the CUDA
-kernels behind the C ABI declared in ``include/gqa.h``.  Tensors are torch
-CUDA tensors (torch provides device memory and streams); there is no CPU or
-library fallback, and importing this module fails loudly when the compiled
-library is missing.
+kernels behind the C ABI declared in ``include/gqa.h``, called through ctypes
+or, where the host's share of a short call counts, through ``_binding``.
+Tensors are torch CUDA tensors (torch provides device memory and streams);
+there is no CPU or library fallback, and importing this module fails loudly
+when the compiled library is missing.
 
 Calls (same names as the C ABI, without the ``gqa_`` prefix):
 
@@ -130,6 +131,20 @@ def _load():
 
 
 lib = _load()
+
+
+def _load_binding():
+    try:
+        from . import _binding as module
+    except ImportError as e:
+        raise ImportError("_binding is not built (%s); run `python kv_cache_decode_04_b200/build.py`" % e) from None
+    module.bind(*(ctypes.cast(getattr(lib, "gqa_" + name), ctypes.c_void_p).value for name in (
+        "prefill_packed", "decode_tree", "cache_append", "cache_compact", "pages_reserve", "pages_fork",
+        "pages_release")), torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    return module
+
+
+_binding = _load_binding()
 
 
 def _check(rc):
@@ -387,23 +402,23 @@ def layer_decode_step(h, W_Q, W_K, W_V, W_O, k_cache, v_cache, seqlens, scale=No
 # ---------------------------------------------------------------- packed prompts, paged caches
 
 
-# These calls are short on the GPU, so what they spend here counts: tensors are checked in one
-# pass, and the current stream is asked for by its handle (0.1 us; torch.cuda.current_stream()
-# builds an object around it in 3 us).
+# These calls are short on the GPU, so what they cost the host counts: _binding (csrc/binding.c)
+# asks the tensors for their device, contiguity and address, finds the stream and calls the
+# library, in a third of the time that this takes through ctypes.
 
 
-_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+def _call(entry, names, stream, *args):
+    """Calls _binding.<entry>(stream, tensors ..., numbers ...); `names` are the tensors'."""
+    rc = entry(stream, *args)
+    if rc != 0:
+        if rc is None:
+            _refuse(names, args)
+        _check(rc)
 
 
-def _ready(names, *tensors):
-    """Every tensor (None: absent) is contiguous and on the current CUDA device, whose index it returns."""
+def _refuse(names, tensors):
+    """Says which tensor is not a contiguous one on the current CUDA device."""
     index = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and not (t.get_device() == index and t.is_contiguous()):
-            break
-    else:
-        if index >= 0 and _current_device() == index:
-            return index
     for name, t in zip(names.split(), tensors):
         if t is None:
             continue
@@ -414,14 +429,6 @@ def _ready(names, *tensors):
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
     raise ValueError("the tensors are on cuda:%d, which is not the current device" % index)
-
-
-def _handle(stream, index):
-    return _current_stream(index) if stream is None else stream.cuda_stream
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
 
 
 _I32 = torch.int32
@@ -443,8 +450,7 @@ def _empty(stream, like, size=None, dtype=None):
 
 
 def _cache(k_cache, v_cache, block_table, B):
-    """(table pointer, G, page, num_pages, M, d_h, dtype code) of a paged cache, or of a dense one
-    without a table."""
+    """(G, page, num_pages, M, d_h, dtype code) of a paged cache, or of a dense one without a table."""
     shape, dtype = k_cache.shape, k_cache.dtype
     if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not dtype:
         raise ValueError("k_cache and v_cache must share a 4-d shape and a dtype")
@@ -453,11 +459,11 @@ def _cache(k_cache, v_cache, block_table, B):
     if block_table is None:
         if P != B:
             raise ValueError("a dense cache must be [B, G, T_cap, d_h] with B = %d" % B)
-        return None, G, page, P, 1, d_h, code
+        return G, page, P, 1, d_h, code
     rows = block_table.shape
     if block_table.dtype is not _I32 or len(rows) != 2 or rows[0] != B:
         raise ValueError("block_table must be int32 [B, M] with B = %d" % B)
-    return block_table.data_ptr(), G, page, P, rows[1], d_h, code
+    return G, page, P, rows[1], d_h, code
 
 
 def prefill_packed(q, k, v, cu_seqlens, scale=None, out=None, stream=None, window=0):
@@ -480,10 +486,8 @@ def prefill_packed(q, k, v, cu_seqlens, scale=None, out=None, stream=None, windo
         out = _empty(stream, q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
-    index = _ready("q k v cu_seqlens out", q, k, v, cu_seqlens, out)
-    _check(lib.gqa_prefill_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), out.data_ptr(), B,
-                                  N, H, G, d_h, 1.0 / math.sqrt(d_h) if scale is None else scale, window, code,
-                                  _handle(stream, index)))
+    _call(_binding.prefill_packed, "q k v cu_seqlens out", stream, q, k, v, cu_seqlens, out, B, N, H, G, d_h, window,
+          code, 1.0 / math.sqrt(d_h) if scale is None else scale)
     return out
 
 
@@ -510,7 +514,7 @@ def decode_tree(q, k_cache, v_cache, seqlens, tree_mask=None, n_draft=None, bloc
     are left as they were.
     """
     B, n, H, d_h = q.shape
-    table, G, page, P, M, d_c, code = _cache(k_cache, v_cache, block_table, B)
+    G, page, P, M, d_c, code = _cache(k_cache, v_cache, block_table, B)
     if d_c != d_h:
         raise ValueError("q and the caches disagree on d_h")
     if q.dtype is not k_cache.dtype:
@@ -524,17 +528,17 @@ def decode_tree(q, k_cache, v_cache, seqlens, tree_mask=None, n_draft=None, bloc
         out = _empty(stream, q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
-    index = _ready("q k_cache v_cache seqlens tree_mask n_draft block_table out workspace", q, k_cache, v_cache,
-                   seqlens, tree_mask, n_draft, block_table, out, workspace)
     if workspace is None:
+        index = q.get_device()
+        if index < 0:
+            raise TypeError("q must be a CUDA tensor")
         size = _tree_workspace(index, B, n, H, G, d_h)
         workspace = _empty(stream, q, size, torch.uint8)
     else:
         size = workspace.numel() * workspace.element_size()
-    _check(lib.gqa_decode_tree(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, seqlens.data_ptr(),
-                               _ptr(tree_mask), _ptr(n_draft), 1.0 / math.sqrt(d_h) if scale is None else scale,
-                               out.data_ptr(), B, n, H, G, d_h, page, P, M, code, workspace.data_ptr(), size,
-                               _handle(stream, index)))
+    _call(_binding.decode_tree, "q k_cache v_cache block_table seqlens tree_mask n_draft out workspace", stream, q,
+          k_cache, v_cache, block_table, seqlens, tree_mask, n_draft, out, workspace, B, n, H, G, d_h, page, P, M,
+          code, size, 1.0 / math.sqrt(d_h) if scale is None else scale)
     return out
 
 
@@ -545,7 +549,7 @@ def cache_append(k_new, v_new, cu_seqlens, seqlens, k_cache, v_cache, block_tabl
     Returns seqlens_out [B] = seqlens + the rows of each.  block_table None: dense caches.
     """
     B = seqlens.numel()
-    table, G, page, P, M, d_h, code = _cache(k_cache, v_cache, block_table, B)
+    G, page, P, M, d_h, code = _cache(k_cache, v_cache, block_table, B)
     rows, dtype = k_new.shape, k_cache.dtype
     N = rows[0]
     if rows != (N, G, d_h) or v_new.shape != rows:
@@ -558,11 +562,9 @@ def cache_append(k_new, v_new, cu_seqlens, seqlens, k_cache, v_cache, block_tabl
         seqlens_out = _empty(stream, seqlens)
     else:
         _int32("seqlens_out", seqlens_out, B)
-    index = _ready("k_cache v_cache k_new v_new cu_seqlens seqlens seqlens_out block_table", k_cache, v_cache, k_new,
-                   v_new, cu_seqlens, seqlens, seqlens_out, block_table)
-    _check(lib.gqa_cache_append(k_new.data_ptr(), v_new.data_ptr(), cu_seqlens.data_ptr(), seqlens.data_ptr(),
-                                seqlens_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table, B, N, G, d_h,
-                                page, P, M, code, _handle(stream, index)))
+    _call(_binding.cache_append, "k_cache v_cache k_new v_new cu_seqlens seqlens seqlens_out block_table", stream,
+          k_cache, v_cache, k_new, v_new, cu_seqlens, seqlens, seqlens_out, block_table, B, N, G, d_h, page, P, M,
+          code)
     return seqlens_out
 
 
@@ -573,7 +575,7 @@ def cache_compact(k_cache, v_cache, seqlens, keep, n_keep=None, block_table=None
     Returns seqlens_out [B] = seqlens + n_keep.  block_table None: dense caches.
     """
     B = seqlens.numel()
-    table, G, page, P, M, d_h, code = _cache(k_cache, v_cache, block_table, B)
+    G, page, P, M, d_h, code = _cache(k_cache, v_cache, block_table, B)
     _int32("seqlens", seqlens, B)
     m = keep.shape[1] if keep.dim() == 2 else 0
     _int32("keep", keep, B, m)
@@ -583,11 +585,8 @@ def cache_compact(k_cache, v_cache, seqlens, keep, n_keep=None, block_table=None
         seqlens_out = _empty(stream, seqlens)
     else:
         _int32("seqlens_out", seqlens_out, B)
-    index = _ready("k_cache v_cache seqlens keep n_keep seqlens_out block_table", k_cache, v_cache, seqlens, keep,
-                   n_keep, seqlens_out, block_table)
-    _check(lib.gqa_cache_compact(k_cache.data_ptr(), v_cache.data_ptr(), table, seqlens.data_ptr(), keep.data_ptr(),
-                                 _ptr(n_keep), seqlens_out.data_ptr(), B, m, G, d_h, page, P, M, code,
-                                 _handle(stream, index)))
+    _call(_binding.cache_compact, "k_cache v_cache block_table seqlens keep n_keep seqlens_out", stream, k_cache,
+          v_cache, block_table, seqlens, keep, n_keep, seqlens_out, B, m, G, d_h, page, P, M, code)
     return seqlens_out
 
 
@@ -610,21 +609,18 @@ def pages_reserve(block_table, refcount, seqlens, n_new, k_pages, v_pages, works
     taken from the pool (lowest free page first, in table order), shared ones are replaced by a copy.
     block_table [B,M] and refcount [P] int32 are updated in place.  All or nothing."""
     B, _, P = _pool(block_table, refcount)
-    table, G, page, pages, M, d_h, code = _cache(k_pages, v_pages, block_table, B)
+    G, page, pages, M, d_h, code = _cache(k_pages, v_pages, block_table, B)
     if pages != P:
         raise ValueError("refcount must hold one count per page (%d)" % pages)
     _int32("seqlens", seqlens, B)
     _int32("n_new", n_new, B)
-    index = _ready("k_pages v_pages block_table refcount seqlens n_new workspace", k_pages, v_pages, block_table,
-                   refcount, seqlens, n_new, workspace)
     if workspace is None:
         size = _reserve_workspace(B, P)
         workspace = _empty(stream, k_pages, size, torch.uint8)
     else:
         size = workspace.numel() * workspace.element_size()
-    _check(lib.gqa_pages_reserve(table, refcount.data_ptr(), seqlens.data_ptr(), n_new.data_ptr(),
-                                 k_pages.data_ptr(), v_pages.data_ptr(), B, G, d_h, page, P, M, code,
-                                 workspace.data_ptr(), size, _handle(stream, index)))
+    _call(_binding.pages_reserve, "block_table refcount seqlens n_new k_pages v_pages workspace", stream, block_table,
+          refcount, seqlens, n_new, k_pages, v_pages, workspace, B, G, d_h, page, P, M, code, size)
 
 
 def pages_fork(block_table, refcount, seqlens, src, dst, page_size, stream=None):
@@ -635,18 +631,16 @@ def pages_fork(block_table, refcount, seqlens, src, dst, page_size, stream=None)
     n = src.numel()
     _int32("src", src, n)
     _int32("dst", dst, n)
-    index = _ready("block_table refcount seqlens src dst", block_table, refcount, seqlens, src, dst)
-    _check(lib.gqa_pages_fork(block_table.data_ptr(), refcount.data_ptr(), seqlens.data_ptr(), src.data_ptr(),
-                              dst.data_ptr(), n, B, page_size, P, M, _handle(stream, index)))
+    _call(_binding.pages_fork, "block_table refcount seqlens src dst", stream, block_table, refcount, seqlens, src, dst,
+          n, B, page_size, P, M)
 
 
 def pages_release(block_table, refcount, lengths, page_size, stream=None):
     """Gives back the pages that lengths[b] positions of each sequence do not need (0: all of them)."""
     B, M, P = _pool(block_table, refcount)
     _int32("lengths", lengths, B)
-    index = _ready("block_table refcount lengths", block_table, refcount, lengths)
-    _check(lib.gqa_pages_release(block_table.data_ptr(), refcount.data_ptr(), lengths.data_ptr(), B, page_size, P, M,
-                                 _handle(stream, index)))
+    _call(_binding.pages_release, "block_table refcount lengths", stream, block_table, refcount, lengths, B, page_size,
+          P, M)
 
 
 def get_status(stream=None):

@@ -1,10 +1,12 @@
-"""Builds libgqa.so in-tree with nvcc for sm_100a (no torch in the link)."""
+"""Builds libgqa.so in-tree with nvcc for sm_100a, and the binding's C part _binding.so with the C
+compiler (no torch in either link)."""
 from __future__ import annotations
 
 import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -13,6 +15,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgqa.so")
 # the same library with the device-side index checks compiled in (-DGQA_DEBUG)
 LIB_DEBUG = os.path.join(PKG, "libgqa_debug.so")
+# the CPython side of the short calls
+BINDING = os.path.join(PKG, "_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.c")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -53,9 +58,25 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
     return lib
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compiles _binding.so unless it is newer than its source and the header."""
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "gqa.h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return BINDING
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-o", tmp, BINDING_SRC]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build_all(force: bool = False, verbose: bool = False) -> None:
-    """Both libraries, compiled side by side."""
+    """Both libraries, compiled side by side, and the binding."""
     import threading
+    build_binding(force=force, verbose=verbose)
     errs = []
 
     def one(debug):
@@ -74,6 +95,7 @@ def build_all(force: bool = False, verbose: bool = False) -> None:
 
 
 if __name__ == "__main__":
+    build_binding(force="--force" in sys.argv, verbose=True)
     if "--debug" in sys.argv:
         build(force="--force" in sys.argv, verbose=True, debug=True)
     else:

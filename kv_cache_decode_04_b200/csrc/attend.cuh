@@ -32,10 +32,11 @@
 // overwrites its S block; the S of a later tile is issued behind the P.V that
 // reads that P, and MMAs of one thread complete in order.
 //
-// What bounds it: one key tile of two row tiles is 2,048 cycles of tensor time
-// and takes about 3,600, the period of one row tile's chain S -> softmax -> P
-// -> P.V (as in prefill.cu).  With one row tile the two parities overlap and a
-// tile takes the 2,430 cycles that HBM needs for its 64 KB.
+// What bounds it (d_h = 128): one key tile of two row tiles is 2,048 cycles of
+// tensor time and takes 3,990, two groups of 16 MMAs at 80-125 cycles each
+// beside the other row tile's softmax: 975 TFLOP/s on 2 x 8192 tokens and 64
+// heads, the rate of prefill.cu.  With one row tile the two parities overlap and
+// a tile takes the 2,430 cycles that HBM needs for its 64 KB (7.4 TB/s).
 #pragma once
 
 #include "common.cuh"
