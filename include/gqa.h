@@ -404,9 +404,10 @@ GQA_API int gqa_decode_tree(const void *q, const void *k_cache, const void *v_ca
  * positions seqlens[b], seqlens[b] + 1, ... of sequence b, and seqlens_out[b] =
  * seqlens[b] + their number.  A sequence without room for all its rows (or with
  * a bad range) gets none, keeps its length and flags GQA_ERR_SEQLEN; rows whose
- * page is missing are not written and flag GQA_ERR_PAGES.  Pages of several
- * rows must be made their own first (gqa_pages_reserve).
- * seqlens_out must not overlap seqlens.  bf16 or fp32, d_h 64 or 128, any page.
+ * page is missing are not written and flag GQA_ERR_PAGES.  Pages that several
+ * rows share must be made the writer's own first (gqa_pages_reserve).
+ * N >= 1; seqlens_out must not overlap seqlens or cu_seqlens, nor the caches one
+ * another or the new rows.  bf16 or fp32, d_h 64 or 128, any page.
  */
 GQA_API int gqa_cache_append(const void *k_new, const void *v_new, const int32_t *cu_seqlens, const int32_t *seqlens,
                              int32_t *seqlens_out, void *k_cache, void *v_cache, const int32_t *block_table, int B,
@@ -421,8 +422,9 @@ GQA_API int gqa_cache_append(const void *k_new, const void *v_new, const int32_t
  * before the call, so any order and repetition of `keep` [B, m] int32 works.
  * Entries lie in [0, 64); n_keep [B] int32 in [0, m], or NULL: m for all.  A
  * sequence with an entry, count or position out of range (GQA_ERR_SEQLEN) or a
- * page missing (GQA_ERR_PAGES) is left as it was.  1 <= m <= 64.  seqlens_out
- * must not overlap seqlens.  bf16 or fp32, d_h 64 or 128, any page.
+ * page missing (GQA_ERR_PAGES) is left as it was.  The rows written must lie in
+ * pages of the sequence's own.  1 <= m <= 64.  seqlens_out must not overlap
+ * seqlens.  bf16 or fp32, d_h 64 or 128, any page.
  */
 GQA_API int gqa_cache_compact(void *k_cache, void *v_cache, const int32_t *block_table, const int32_t *seqlens,
                               const int32_t *keep, const int32_t *n_keep, int32_t *seqlens_out, int B, int m, int G,
