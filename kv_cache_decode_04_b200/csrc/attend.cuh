@@ -124,7 +124,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64
 //     wrote O is complete, because the S just read was issued behind it.
 //   - m = -inf (no key seen yet): every score is -inf and p = 0.
 //   - The row sum adds the unrounded p in fp32.
-// Moves the maximum to cover mx (raw scores; the scale is positive).
+// softmax_whole and softmax_part below do this for the two kinds of tile.
+
+// Moves the maximum to cover mx (log2 units) and rescales l and O with it.
 template <int D>
 __device__ __forceinline__ void move_max(uint32_t tO, float mx, bool first, float &m, float &l) {
     if (first) {
