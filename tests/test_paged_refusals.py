@@ -120,3 +120,15 @@ def test_the_binding_checks_shapes_types_and_devices():
         gqa.pages_reserve(i(2, 4), i(6), i(2), i(2), z(5, 2, 16, 64), z(5, 2, 16, 64))
     with pytest.raises(ValueError):
         gqa.pages_fork(i(2, 4), i(6), i(2), i(2), i(1), page_size=16)
+
+
+def test_pages_reserve_page_of_2g_pieces():
+    # the copy of a shared page counts its 16-byte pieces, 16 a row here, in 32 bits
+    big = dict(k=1 << 41, v=1 << 42, B=2, G=8, d_h=128, P=2, M=1)
+
+    def reserve(page):
+        return L.gqa_pages_reserve(A, BB, C, D, big["k"], big["v"], big["B"], big["G"], big["d_h"], page, big["P"],
+                                   big["M"], gqa.GQA_BF16, G_, 0, None)
+
+    assert reserve(1 << 24) == -2
+    assert reserve(1 << 23) == -5  # only the workspace is missing
