@@ -695,7 +695,8 @@ int gqa_decode_tree(const void *q, const void *k_cache, const void *v_cache, con
     if (block_table && page % 16) return fail(GQA_ERR_UNSUPPORTED, "page=%d must be a multiple of 16", page);
     if (B > 8000) return fail(GQA_ERR_UNSUPPORTED, "tree decode needs B <= 8000 (got %d)", B);
     const long long pt = 128 / r, blocks = (n + pt - 1) / pt;
-    if ((long long)B * G * blocks * ((c.cap + 127ll) / 128 + 2) >= (1ll << 31) || (long long)B * n * H >= (1ll << 31))
+    // a segment counts up to 3 tiles more than it has
+    if ((long long)B * G * blocks * ((c.cap + 127ll) / 128 + 3) >= (1ll << 31) || (long long)B * n * H >= (1ll << 31))
         return fail(GQA_ERR_UNSUPPORTED, "too many key tiles or query rows for one call");
     if (misaligned(q, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(out, 16) ||
         misaligned(seqlens, 4) || misaligned(tree_mask, 8) || misaligned(n_draft, 4))

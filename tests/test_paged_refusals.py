@@ -132,3 +132,9 @@ def test_pages_reserve_page_of_2g_pieces():
 
     assert reserve(1 << 24) == -2
     assert reserve(1 << 23) == -5  # only the workspace is missing
+
+
+def test_decode_tree_line_of_2g_tiles():
+    # 2^29 segments of one tile, each counted as four
+    kw = dict(q=1 << 48, k=1 << 49, v=1 << 50, out=1 << 51, B=1 << 12, n=1, P=1, M=1, page=16, wsb=0)
+    assert tree(**kw, H=1 << 17, G=1 << 17) == -2
