@@ -441,7 +441,8 @@ GQA_API int gqa_cache_compact(void *k_cache, void *v_cache, const int32_t *block
  * flagged.  A sequence whose range is negative or beyond its capacity is
  * skipped and flags GQA_ERR_SEQLEN.
  *   workspace >= gqa_pages_reserve_workspace_bytes(B, num_pages), 256-byte aligned
- * Supported: bf16 or fp32, d_h 64 or 128, B <= 8192, pages below 2^35 bytes.
+ * Supported: bf16 or fp32, d_h 64 or 128, B <= 8192, B*M < 2^31 table entries,
+ * pages below 2^35 bytes.
  */
 GQA_API size_t gqa_pages_reserve_workspace_bytes(int B, int num_pages);
 GQA_API int gqa_pages_reserve(int32_t *block_table, int32_t *refcount, const int32_t *seqlens, const int32_t *n_new,

@@ -839,6 +839,8 @@ int gqa_pages_reserve(int32_t *block_table, int32_t *refcount, const int32_t *se
     rc = cache_view(&c, block_table, B, G, d_h, page, num_pages, M, dt);
     if (rc) return rc;
     if (!seqlens || !n_new || !k_pages || !v_pages) return fail(GQA_ERR_INVALID, "null tensor pointer");
+    if ((long long)B * M > INT32_MAX)  // the plan counts the entries that need a page in 32 bits
+        return fail(GQA_ERR_UNSUPPORTED, "B*M must be below 2^31 table entries");
     if ((long long)G * page * c.row16 > INT32_MAX - 256)  // the copy of a page counts its pieces in 32 bits
         return fail(GQA_ERR_UNSUPPORTED, "a page must stay below 2^35 bytes");
     if (overlaps(k_pages, cache_bytes(c), v_pages, cache_bytes(c)))

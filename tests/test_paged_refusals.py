@@ -138,3 +138,15 @@ def test_decode_tree_line_of_2g_tiles():
     # 2^29 segments of one tile, each counted as four
     kw = dict(q=1 << 48, k=1 << 49, v=1 << 50, out=1 << 51, B=1 << 12, n=1, P=1, M=1, page=16, wsb=0)
     assert tree(**kw, H=1 << 17, G=1 << 17) == -2
+
+
+def test_pages_reserve_table_of_2g_entries():
+    # the plan counts the entries that need a page in 32 bits
+    def reserve(B, M, page=16):
+        return L.gqa_pages_reserve(1 << 50, 1 << 51, C, D, 1 << 52, 1 << 53, B, 2, 64, page, 10, M, gqa.GQA_BF16, G_, 0,
+                                   None)
+
+    assert reserve(17, 134217711) == -2
+    assert reserve(8192, 1 << 18, 1) == -2
+    assert reserve(8192, (1 << 18) - 1, 1) == -5  # only the workspace is missing
+    assert reserve(1, 134217711) == -5
