@@ -402,10 +402,12 @@ GQA_API int gqa_decode_tree(const void *q, const void *k_cache, const void *v_ca
  * gqa_cache_append -- writes new tokens' keys and values into a cache: rows
  * cu_seqlens[b] .. cu_seqlens[b+1] - 1 of k_new, v_new [N, G, d_h] go to
  * positions seqlens[b], seqlens[b] + 1, ... of sequence b, and seqlens_out[b] =
- * seqlens[b] + their number.  A sequence without room for all its rows (or with
- * a bad range) gets none, keeps its length and flags GQA_ERR_SEQLEN; rows whose
- * page is missing are not written and flag GQA_ERR_PAGES.  Pages that several
- * rows share must be made the writer's own first (gqa_pages_reserve).
+ * seqlens[b] + their number.  A sequence without room for all its rows, or whose
+ * range is not 0 <= cu_seqlens[b] <= cu_seqlens[b+1] <= N or begins below an
+ * earlier offset, gets none, keeps its length and flags GQA_ERR_SEQLEN; rows whose
+ * page is missing are not written (their number counts all the same) and flag
+ * GQA_ERR_PAGES.  Pages that several rows share must be made the writer's own
+ * first (gqa_pages_reserve).
  * N >= 1; seqlens_out must not overlap seqlens or cu_seqlens, nor the caches one
  * another or the new rows.  bf16 or fp32, d_h 64 or 128, any page.
  */

@@ -43,10 +43,42 @@ __device__ __forceinline__ size_t piece_of(const CacheView &c, int page, int g, 
 constexpr int kAppendWarps = 8;
 constexpr int kAppendHeld = 4;  // pieces of K and of V that a lane has in flight
 
+// Whether some entry of cu[0 .. B] is below the one before it: each thread of
+// the block looks at its part.  Four entries a load, the next thread's first by
+// shuffle, since at 8192 sequences what the blocks of an SM read here adds up.
+__device__ __forceinline__ bool any_falls(const int32_t *cu, int B) {
+    const bool wide = (reinterpret_cast<uintptr_t>(cu) & 15) == 0;
+    bool falls = false;
+    for (int base = 0; base <= B; base += blockDim.x * 4) {
+        const int i = base + threadIdx.x * 4;
+        int4 x = make_int4(INT_MAX, INT_MAX, INT_MAX, INT_MAX);  // entries behind the last
+        if (wide && i + 3 <= B) {
+            x = *reinterpret_cast<const int4 *>(cu + i);
+        } else {
+            if (i <= B) x.x = cu[i];
+            if (i + 1 <= B) x.y = cu[i + 1];
+            if (i + 2 <= B) x.z = cu[i + 2];
+            if (i + 3 <= B) x.w = cu[i + 3];
+        }
+        int next = __shfl_down_sync(0xffffffffu, x.x, 1);
+        if ((threadIdx.x & 31) == 31) next = i + 4 <= B ? cu[i + 4] : INT_MAX;
+        falls = falls || x.y < x.x || x.z < x.y || x.w < x.z || next < x.w;
+    }
+    return falls;
+}
+
 // One warp per new token: it finds the token's sequence in cu_seqlens (a
 // binary search over B + 1 entries), then moves the token's G rows of K and of
 // V, all loads of a round before its stores.  HBM-bound for prompts: each byte
 // is read once and written once.
+//
+// A sequence is served, all its rows and its length, or left alone: it is left
+// alone when its range is bad, when it has no room, or when it begins below an
+// earlier offset, so the served ranges never share a row.  Offsets that fall
+// are rare and found by every block at its start (the entries are the ones the
+// search then reads); only then is an earlier offset looked for, and the search
+// linear: a range that is served holds tok exactly when the first offset above
+// tok is its end.
 __global__ void __launch_bounds__(kAppendWarps * 32)
     cache_append_kernel(const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new, const int32_t *cu,
                         const int32_t *seqlens, int32_t *seqlens_out, uint4 *__restrict__ k_cache,
@@ -54,27 +86,37 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
     pdl_wait_primary();
     const int lane = threadIdx.x & 31;
     const int gid = blockIdx.x * blockDim.x + threadIdx.x;
-    // lengths after the append, and the checks of each sequence (once, here)
+    const bool falls = __syncthreads_or(any_falls(cu, c.B));
+    auto served = [&](int b, int lo, int hi, int T) {
+        if (lo < 0 || hi < lo || hi > N || T < 0 || hi - lo > c.cap || T > c.cap - (hi - lo)) return false;
+        if (falls)
+            for (int i = 0; i < b; ++i)
+                if (cu[i] > lo) return false;
+        return true;
+    };
+    // lengths after the append (once, here)
     for (int b = gid; b < c.B; b += gridDim.x * blockDim.x) {
         const int lo = cu[b], hi = cu[b + 1], T = seqlens[b];
-        const bool ok = lo >= 0 && hi >= lo && hi <= N && T >= 0 && hi - lo <= c.cap && T <= c.cap - (hi - lo);
+        const bool ok = served(b, lo, hi, T);
         if (!ok) set_status(status, STATUS_SEQLEN);
         seqlens_out[b] = ok ? T + (hi - lo) : T;
     }
-    const int end = min(N, max(0, cu[c.B]));
+    const int end = falls ? N : min(N, max(0, cu[c.B]));
     const int pieces = c.G * c.row16;
     const int shift = __ffs(c.row16) - 1;  // pieces of a row: 8, 16 or 32
     for (int tok = gid >> 5; tok < end; tok += (gridDim.x * blockDim.x) >> 5) {
         int lo = 0, hi = c.B - 1;  // the last b with cu[b] <= tok
+        if (falls) {
+            while (lo < c.B && cu[lo + 1] <= tok) ++lo;  // cu[0] > tok: its range does not hold tok
+            if (lo == c.B) continue;
+            hi = lo;
+        }
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (cu[mid] <= tok) lo = mid; else hi = mid - 1;
         }
         const int first = cu[lo], last = cu[lo + 1], T = seqlens[lo];
-        // not in this sequence after all (a cu_seqlens that falls), or no room for its rows
-        if (first < 0 || tok < first || tok >= last || last > N || T < 0 || last - first > c.cap ||
-            T > c.cap - (last - first))
-            continue;
+        if (tok < first || tok >= last || !served(lo, first, last, T)) continue;
         int page, row;
         if (!locate(c, lo, T + tok - first, page, row)) {
             if (lane == 0) set_status(status, STATUS_PAGES);

@@ -317,3 +317,52 @@ def test_a_pool_step_replays(gqa):
     torch.cuda.synchronize()
     x.check()
     gqa.get_status()
+
+
+def broken(counts, N, gen, spots):
+    """Offsets of these counts with `spots` entries replaced by anything from -2 to N + 2."""
+    cu = [sum(counts[:b]) for b in range(len(counts) + 1)]
+    for _ in range(spots):
+        at = int(torch.randint(0, len(cu), (1,), generator=gen))
+        cu[at] = int(torch.randint(-2, N + 3, (1,), generator=gen))
+    return cu
+
+
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("cu,lens", [([0, 40, 20], [3, 5]), ([0, 10, 5, 15], [0, 1, 2]), ([20, 0, 40], [0, 0]),
+                                     (5, None), (70, None), (300, None)])
+def test_append_offsets_that_fall(gqa, page, cu, lens):
+    """A sequence is served, all its rows and its length, unless its own range is bad or begins below an
+    earlier offset; no length counts a row that was not written."""
+    G, d, cap = 2, 64, 80
+    gen = torch.Generator().manual_seed(1 if lens else cu)
+    trials = [(cu, lens)]
+    if lens is None:
+        trials = []
+        for spots in (1, 2, 3, 8):
+            counts = torch.randint(0, 9, (cu,), generator=gen).tolist()
+            trials.append((broken(counts, sum(counts), gen, spots),
+                           torch.randint(0, cap - 4, (cu,), generator=gen).tolist()))
+    for offsets, T in trials:
+        B = len(T)
+        N = max(1, min(max(offsets), 2000))
+        k, v, table = caches(B, G, d, page, cap, torch.bfloat16, seed=B)
+        kn, vn = (torch.randn((N, G, d), generator=gen).to(torch.bfloat16) for _ in range(2))
+        kd, vd = k.cuda(), v.cuda()
+        got = gqa.cache_append(kn.cuda(), vn.cuda(), i32(offsets), i32(T), kd, vd,
+                               block_table=None if table is None else table.cuda())
+        want, bad = list(T), False
+        for b in range(B):
+            lo, hi = offsets[b], offsets[b + 1]
+            if not (0 <= lo <= hi <= N and lo >= max(offsets[:b + 1]) and T[b] + hi - lo <= cap):
+                bad = True
+                continue
+            want[b] += hi - lo
+            for i in range(hi - lo):
+                p, r = ref.place(table, page, b, T[b] + i)
+                k[p, :, r], v[p, :, r] = kn[lo + i], vn[lo + i]
+        assert got.tolist() == want
+        assert same(kd, k) and same(vd, v)
+        if bad:
+            expect(gqa, -7)
+        gqa.get_status()
