@@ -347,8 +347,9 @@ GQA_API int gqa_layer_decode_step(const void *h, const void *W_Q, const void *W_
  *   q, out      device, [N, H, d_h]; k, v device, [N, G, d_h]; bf16, 16-byte
  *               aligned; out must not overlap an input
  *   cu_seqlens  device, [B+1] int32, 0 <= cu_seqlens[b] <= cu_seqlens[b+1] <= N;
- *               empty sequences are allowed.  Entries out of range or falling
- *               are clamped and flag GQA_ERR_SEQLEN.
+ *               empty sequences are allowed.  Entries out of range are clamped
+ *               to it, one below an earlier entry counts as the largest before
+ *               it (so sequences never overlap), and both flag GQA_ERR_SEQLEN.
  * Rows of out that belong to no sequence are left as they were, and no
  * sequence's result depends on another's values, or on those of such rows.
  * Supported: bf16, d_h 64 or 128, H/G <= 128, B <= 8192, N*H < 2^31; scale

@@ -53,6 +53,7 @@ struct PackedPolicy {
     int4 *ring;           // [kRing] (first packed position, length, first position, group); group < 0: no more
     uint64_t *filled, *taken;  // [kRing]
     int *counts;          // [B] pieces of each sequence (per group)
+    bool falls;           // some entry of cu is below the one before it
     volatile int *vabort;
     unsigned *status;
     float scale_log2;
@@ -67,10 +68,15 @@ struct PackedPolicy {
         int pos, key_lo, out_row;
     };
 
-    // Start and length of sequence b, forced into [0, N].
-    static __device__ __forceinline__ int2 span(const PackedParams &p, int b) {
-        const int a = min(max(p.cu[b], 0), p.N);
-        return make_int2(a, min(max(p.cu[b + 1], a), p.N) - a);
+    // Start and length of sequence b: offsets are forced into [0, N] and, where some fall, up to
+    // the largest before them, so that no row belongs to two sequences.
+    static __device__ __forceinline__ int2 span(const PackedParams &p, int b, bool falls) {
+        int a = min(max(p.cu[b], 0), p.N);
+        if (falls) {
+#pragma unroll 1
+            for (int i = 0; i < b; ++i) a = max(a, min(p.cu[i], p.N));
+        }
+        return make_int2(a, max(min(p.cu[b + 1], p.N), a) - a);
     }
 
     // The consumers of a ring entry: the two TMA warps, the two MMA threads, the softmax warps.
@@ -201,7 +207,7 @@ struct PackedPolicy {
                 if (k < n) {
                     found = ((has >> lane) & 1u) && __popc(has & ((1u << lane) - 1u)) == k;
                     if (found) {
-                        const int2 w = span(p, b);
+                        const int2 w = span(p, b, falls);
                         e = make_int4(w.x, w.y, s.x * p2, u - v * p.G);
                     }
                     break;
@@ -261,18 +267,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) tc::tmem_alloc(bar.tmem_slot, kTmemCols);
     tc::fence_before();
     pdl_wait_primary();
+    auto count = [&](int b, bool falls) {
+        return (PackedPolicy<D>::span(p, b, falls).y + 2 * p.pt - 1) / (2 * p.pt);
+    };
+    bool falls = false;
     for (int b = threadIdx.x; b < p.B; b += kThreads) {
-        const int2 s = PackedPolicy<D>::span(p, b);
-        counts[b] = (s.y + 2 * p.pt - 1) / (2 * p.pt);
         const int a = p.cu[b], z = p.cu[b + 1];
+        counts[b] = count(b, false);
+        falls = falls || z < a;
         if (blockIdx.x == 0 && (a < 0 || z < a || z > p.N)) set_status(p.status, STATUS_SEQLEN);
     }
-    __syncthreads();
+    falls = __syncthreads_or(falls);
+    if (falls) {
+        for (int b = threadIdx.x; b < p.B; b += kThreads) counts[b] = count(b, true);
+        __syncthreads();
+    }
     tc::fence_after();
     const uint32_t tmem = *bar.tmem_slot;
-    PackedPolicy<D> pol{p, &tmq, &tmk, &tmv, ring, bar.policy, bar.policy + kRing, counts, bar.abort_flag, p.status,
-                        p.scale_log2, static_cast<__nv_bfloat16 *>(p.out), p.timeout_ns, l2_policy_evict_first(),
-                        l2_policy_evict_last()};
+    PackedPolicy<D> pol{p, &tmq, &tmk, &tmv, ring, bar.policy, bar.policy + kRing, counts, falls, bar.abort_flag,
+                        p.status, p.scale_log2, static_cast<__nv_bfloat16 *>(p.out), p.timeout_ns,
+                        l2_policy_evict_first(), l2_policy_evict_last()};
     attend<D, 1>(pol, sm, tmem);
     tc::fence_before();
     __syncthreads();

@@ -170,3 +170,40 @@ def test_captured_replayed_and_on_another_stream(gqa):
     torch.cuda.synchronize()
     assert torch.equal(out, gqa.prefill_packed(q, k, v, cu))
     gqa.get_status()
+
+
+@pytest.mark.parametrize("cu,held", [
+    ([-5, 300], [0, 300]), ([0, 301], [0, 300]), ([0, 1 << 30], [0, 300]), ([0, 200, 100, 300], [0, 200, 200, 300]),
+    ([50, 20, 10, 250], [50, 50, 50, 250]), ([0, 1 << 30, 5, 300], [0, 300, 300, 300]),
+    ([-5, 100, -7, 200], [0, 100, 100, 200]), ([0, 150, 0, 150, 0, 290], [0, 150, 150, 150, 150, 290]),
+    ([0, 60, 130] + [129, 131] * 200 + [280], [0, 60, 130] + [130] + [131] * 399 + [280])])
+@pytest.mark.parametrize("H,G", [(4, 2), (3, 1)])
+def test_bad_offsets_count_as_the_largest_before_them(gqa, H, G, cu, held):
+    """Offsets are forced into [0, N] and then up to the largest before them: no row has two sequences."""
+    q, k, v = inputs([0, 300], H, G, 64, seed=13)
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    gqa.prefill_packed(q.cuda(), k.cuda(), v.cuda(), torch.tensor(cu, dtype=torch.int32).cuda(), out=out)
+    with pytest.raises(gqa.GQAError) as e:
+        gqa.get_status()
+    assert e.value.code == -7
+    gqa.get_status()
+    r, w = ref.prefill_packed(q, k, v, held, 64 ** -0.5)
+    compare(out.cpu(), r, w, q)
+
+
+def test_offsets_that_fall_in_the_largest_batch(gqa):
+    lens = [b % 4 for b in range(8192)]
+    cu = offsets(lens)
+    q, k, v = inputs(cu, 2, 1, 64, seed=16)
+    bad = list(cu)
+    bad[1] = 700
+    bad[4000] = bad[6000] = 5
+    held = [max(bad[:b + 1]) for b in range(8193)]
+    want = run(gqa, q, k, v, held)
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    gqa.prefill_packed(q.cuda(), k.cuda(), v.cuda(), torch.tensor(bad, dtype=torch.int32).cuda(), out=out)
+    with pytest.raises(gqa.GQAError) as e:
+        gqa.get_status()
+    assert e.value.code == -7
+    assert torch.equal(out.cpu(), want)
+    gqa.get_status()
