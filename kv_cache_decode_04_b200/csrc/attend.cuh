@@ -328,7 +328,6 @@ struct PieceBase {
     // keys of row tile 0 and 1, from the first key of the piece's first tile on (0:
     // the tile has no rows).  Row tile i visits ceil(k_i / 128) tiles.
     int k0, k1;
-    bool split;  // carry P as two bf16 terms
     __device__ int tiles() const { return (max(k0, k1) + kKeys - 1) / kKeys; }
 };
 
@@ -397,7 +396,8 @@ struct Barriers {
 
 // Everything after set-up: all threads of the CTA, tensor memory allocated at
 // `tmem`.  Pol is the policy:
-//   Pol::Piece                    a PieceBase with more
+//   Pol::Piece                    a PieceBase with more: split(row tile) says whether its P is carried
+//                                 as two bf16 terms
 //   Pol::Iter(pol, whole_warp)    walks the CTA's pieces: bool next(Piece &), the same for all lanes
 //                                 when a whole warp calls it, and done() when the calling role is
 //                                 through with a piece (one call per piece)
@@ -532,7 +532,7 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
                     last = PAIR ? keys <= (v_j + 1) * kKeys : v_j + 2 >= v_n;
                     // how P lies in its S block: 0 as softmax_whole left it, else softmax_part's chunks
                     nch = chunks_of(keys, v_j);
-                    if (nch == 4 && !vq.split && !pol.masked(vq, PAIR ? hh : 0, v_j)) nch = 0;
+                    if (nch == 4 && !vq.split(PAIR ? hh : 0) && !pol.masked(vq, PAIR ? hh : 0, v_j)) nch = 0;
                     if ((PAIR || mine) && !wait(&bar.v_full[vs], (it / ST) & 1)) break;
                 }
                 // the next scores, unless they open a piece: its Q may still be on its way, and
@@ -554,7 +554,7 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
                             tc::mma_ts(tO, tS + kk * 8, d + ((kk * 2048) >> 4), idesc_o, (acc || kk > 0) ? 1u : 0u);
                     } else {
 #pragma unroll 1
-                        for (int lo = 0; lo <= (vq.split ? 16 : 0); lo += 16)
+                        for (int lo = 0; lo <= (vq.split(PAIR ? hh : 0) ? 16 : 0); lo += 16)
 #pragma unroll 1
                             for (int kk = 0; kk < 2 * nch; ++kk)
                                 tc::mma_ts(tO, tS + (kk >> 1) * 32 + (kk & 1) * 8 + lo, d + ((kk * 2048) >> 4),
@@ -737,10 +737,10 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
                 ++cnt;
                 tc::fence_after();
                 const int nch = chunks_of(keys, j);
-                if (nch == 4 && !q.split && !pol.masked(q, PAIR ? hh : 0, j)) {
+                if (nch == 4 && !q.split(PAIR ? hh : 0) && !pol.masked(q, PAIR ? hh : 0, j)) {
                     softmax_whole<D>(tS, tO, pol.scale_log2, first, m, l);
                 } else {
-                    softmax_part<D>(tS, tO, pol.scale_log2, first, q.split, nch, m, l,
+                    softmax_part<D>(tS, tO, pol.scale_log2, first, q.split(PAIR ? hh : 0), nch, m, l,
                                     [&](int c) { return pol.words(q, row, j, c); });
                     // V rows that no row of the piece sees, those past the sequence's end among them:
                     // P is 0 there, but 0 times what they hold must stay 0.  Each warpgroup clears

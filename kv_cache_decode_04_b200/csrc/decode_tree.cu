@@ -113,6 +113,8 @@ struct TreePolicy {
     struct Piece : PieceBase {
         int b, g, rb, T, nd, j0;
         int slot;  // record slot, -1: the segment is whole
+        bool two_terms;
+        __device__ bool split(int) const { return two_terms; }
     };
     struct Row {
         uint64_t bits;  // drafts that the row sees
@@ -154,7 +156,7 @@ struct TreePolicy {
                 q.k0 = keys;
                 q.k1 = PAIR && s.y - q.rb * p.pb > p.pt ? keys : 0;
                 // as in the dense decode: P as two terms for at most 256 positions
-                q.split = n_tok <= 256;
+                q.two_terms = n_tok <= 256;
                 return true;
             }
             return false;

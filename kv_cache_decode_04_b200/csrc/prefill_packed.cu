@@ -63,6 +63,8 @@ struct PackedPolicy {
 
     struct Piece : PieceBase {
         int start, len, s0, g, j_lo;
+        bool split0, split1;
+        __device__ bool split(int hh) const { return hh ? split1 : split0; }
     };
     struct Row {
         int pos, key_lo, out_row;
@@ -109,7 +111,11 @@ struct PackedPolicy {
             const int base = q.j_lo * kKeys;
             q.k0 = min(q.len, q.s0 + p.pt) - base;
             q.k1 = q.s0 + p.pt < q.len ? min(q.len, q.s0 + 2 * p.pt) - base : 0;
-            q.split = base + max(q.k0, q.k1) <= kKeys || (p.window > 0 && p.window <= 256);
+            // as in the dense prefill: P as two terms for the rows of positions 0 to 127 (a tile
+            // that holds one of them) and in narrow windows
+            const bool narrow = p.window > 0 && p.window <= 256;
+            q.split0 = q.s0 < kKeys || narrow;
+            q.split1 = q.s0 + p.pt < kKeys || narrow;
             return true;
         }
         __device__ void done() {

@@ -207,3 +207,27 @@ def test_offsets_that_fall_in_the_largest_batch(gqa):
     assert e.value.code == -7
     assert torch.equal(out.cpu(), want)
     gqa.get_status()
+
+
+@pytest.mark.parametrize("H,G,d", [(4, 4, 64), (2, 2, 128), (4, 2, 128), (6, 2, 64), (8, 2, 64), (5, 1, 128),
+                                   (6, 1, 64), (7, 1, 64), (64, 1, 64), (100, 1, 64)])
+def test_first_rows_carry_p_as_two_terms(gqa, H, G, d):
+    """Positions 0 to 127 of every prompt, whatever its length and group size."""
+    cu = offsets([300, 1, 128, 129, 57, 700])
+    q, k, v = inputs(cu, H, G, d, seed=H + d)
+    got = run(gqa, q, k, v, cu)
+    r, w = ref.prefill_packed(q, k, v, cu, d ** -0.5)
+    compare(got, r, w, q)
+    for a, z in zip(cu[:-1], cu[1:]):
+        z = min(z, a + 128)
+        ref.check(got[a:z], r[a:z], w[a:z], split=True)
+
+
+@pytest.mark.parametrize("window", [1, 2, 3, 31, 127, 128, 200, 256])
+@pytest.mark.parametrize("H,G,d", [(2, 2, 128), (6, 2, 64), (8, 1, 64)])
+def test_narrow_windows_carry_p_as_two_terms(gqa, window, H, G, d):
+    cu = offsets([3, 700, 129])
+    q, k, v = inputs(cu, H, G, d, seed=window)
+    got = run(gqa, q, k, v, cu, window=window)
+    r, w = ref.prefill_packed(q, k, v, cu, d ** -0.5, window)
+    ref.check(got, r, w, split=True)
