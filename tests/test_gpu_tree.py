@@ -250,3 +250,14 @@ def test_graphs_that_share_a_workspace_and_two_streams(gqa):
     for g, w in zip(got, want):
         assert all(torch.equal(y, w) for y in g)
     gqa.get_status()
+
+
+@pytest.mark.parametrize("n,H,G,d", [(1, 4, 4, 64), (1, 8, 1, 128), (8, 8, 2, 128), (16, 8, 1, 64), (64, 2, 2, 64),
+                                     (64, 4, 1, 128), (33, 7, 1, 64)])
+@pytest.mark.parametrize("page", [0, 48])
+def test_short_contexts_carry_p_as_two_terms(gqa, n, H, G, d, page):
+    """Sequences of at most 256 positions, drafts included."""
+    x = Case(5, n, H, G, d, page, [0, 3, 100, 150, 256 - n], seed=n + H + page)
+    got = run(gqa, x)
+    r, w = ref.decode_tree(x.q, x.k, x.v, x.table, x.seqlens, x.mask, x.counts, x.scale)
+    ref.check(got, r, w, split=True)
