@@ -352,6 +352,8 @@ GQA_API int gqa_layer_decode_step(const void *h, const void *W_Q, const void *W_
  *               it (so sequences never overlap), and both flag GQA_ERR_SEQLEN.
  * Rows of out that belong to no sequence are left as they were, and no
  * sequence's result depends on another's values, or on those of such rows.
+ * A row that sees a score that is NaN or +inf is NaN.  (A value of v that is not
+ * finite can reach the rows of its sequence that do not see it yet: 0 * NaN.)
  * Supported: bf16, d_h 64 or 128, H/G <= 128, B <= 8192, N*H < 2^31; scale
  * finite and positive.
  */
@@ -385,9 +387,10 @@ GQA_API int gqa_prefill_packed(const void *q, const void *k, const void *v, cons
  *   workspace   >= gqa_decode_tree_workspace_bytes(...), 256-byte aligned; its
  *               contents need no initialisation and nothing in it is kept
  * Rows out[b, i >= n_draft[b]] are left as they were.  A row that sees nothing
- * is zero.  Positions past T_b + n_draft[b], and drafts that no mask of the
- * sequence names, are never used, whatever they hold.  (A value that is not
- * finite in a position that only some rows see can reach the others: 0 * NaN.)
+ * is zero, one that sees a score that is NaN or +inf is NaN.  Positions past
+ * T_b + n_draft[b], and drafts that no mask of the sequence names, are never
+ * used, whatever they hold.  (A value of V that is not finite in a position that
+ * only some rows see can reach the others: 0 * NaN.)
  * A missing page counts as zeros and flags GQA_ERR_PAGES; lengths and counts out
  * of range are clamped and flag GQA_ERR_SEQLEN.
  * Supported: bf16, d_h 64 or 128, 1 <= n <= 64, H/G <= 128, B <= 8000, page a

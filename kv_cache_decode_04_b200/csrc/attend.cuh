@@ -663,7 +663,8 @@ __device__ __forceinline__ void attend(Pol &pol, uint8_t *sm, uint32_t tmem) {
             }
             if (!PAIR || keys > 0) {
                 if (!rec) {
-                    const float inv = L > 0.f ? 1.f / L : 0.f;
+                    // (L = 0: the row sees nothing; a NaN, from a score that is NaN or +inf, stays one)
+                    const float inv = L == 0.f ? 0.f : 1.f / L;
                     w0 *= inv;
                     w1 *= inv;
                 }

@@ -350,7 +350,10 @@ __global__ void __launch_bounds__(kRows *(PAIR + 1)) decode_tree_combine(const T
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            if (v[j].x == -INFINITY) continue;  // no record, or nothing seen yet
+            if (v[j].x == -INFINITY) {  // no record, or nothing seen yet (0); all that was seen is NaN (NaN)
+                L += v[j].y;
+                continue;
+            }
             const float Mn = fmaxf(M, v[j].x);
             const float a = fast_exp2(M - Mn), w = fast_exp2(v[j].x - Mn);
             L = L * a + w * v[j].y;
@@ -359,7 +362,7 @@ __global__ void __launch_bounds__(kRows *(PAIR + 1)) decode_tree_combine(const T
             M = Mn;
         }
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
     uint32_t pk[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) pk[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);

@@ -231,3 +231,30 @@ def test_narrow_windows_carry_p_as_two_terms(gqa, window, H, G, d):
     got = run(gqa, q, k, v, cu, window=window)
     r, w = ref.prefill_packed(q, k, v, cu, d ** -0.5, window)
     ref.check(got, r, w, split=True)
+
+
+@pytest.mark.parametrize("where", ["q", "k", "v"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("H,G", [(2, 2), (6, 2)])
+def test_a_row_that_sees_a_value_that_is_not_finite_says_so(gqa, where, value, H, G):
+    """One element of one position is not finite: the rows that see it are what the formula makes of it
+    (a score of +inf is NaN, one of -inf counts for nothing), the rows before it what they were."""
+    cu = offsets([40, 400])
+    q, k, v = inputs(cu, H, G, 64, seed=14)
+    at = 40 + 230
+    for x, name in ((q, "q"), (k, "k"), (v, "v")):
+        if name == where:
+            x[at, 0, 5] = value
+    got = run(gqa, q, k, v, cu).double()
+    r, w = ref.prefill_packed(q, k, v, cu, 64 ** -0.5)
+    for b in range(2):
+        for s in range(cu[b], cu[b + 1]):
+            # (0 * NaN: V's own column, in rows before the position)
+            if where == "v" and s < at:
+                r[s, : H // G, 5] = got[s, : H // G, 5]
+                w[s, : H // G, 5] = 0
+    assert torch.equal(torch.isnan(got), torch.isnan(r))
+    assert torch.equal(got[torch.isinf(r)], r[torch.isinf(r)])
+    fine = torch.isfinite(r) & torch.isfinite(got)
+    assert fine.sum() > 0.4 * r.numel() and torch.equal(torch.isfinite(got), torch.isfinite(r))
+    ref.check(got[fine], r[fine], w[fine])

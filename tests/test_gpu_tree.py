@@ -261,3 +261,23 @@ def test_short_contexts_carry_p_as_two_terms(gqa, n, H, G, d, page):
     got = run(gqa, x)
     r, w = ref.decode_tree(x.q, x.k, x.v, x.table, x.seqlens, x.mask, x.counts, x.scale)
     ref.check(got, r, w, split=True)
+
+
+@pytest.mark.parametrize("n,H,G", [(4, 4, 2), (64, 4, 1), (1, 2, 2)])
+@pytest.mark.parametrize("T,at", [(50, 20), (900, 899), (9000, 4000)])
+def test_a_row_that_sees_a_score_that_is_not_finite_says_so(gqa, n, H, G, T, at):
+    """In whole segments and in ones cut over many CTAs: a visible NaN or +inf score gives NaN, one of
+    -inf counts for nothing, and the other heads, rows and sequences are what they were."""
+    nan, inf = float("nan"), float("inf")
+    for where, value in (("q", nan), ("q", inf), ("cached", nan), ("cached", inf), ("cached", -inf), ("draft", nan)):
+        x = Case(2, n, H, G, 64, 64, [T, 70], seed=15)
+        if where == "q":
+            x.q[0, n // 2, 0, 5] = value
+        else:
+            p, i = ref.place(x.table, 64, 0, T + n // 2 if where == "draft" else at)
+            x.k[p, 0, i, 5] = value
+        got = run(gqa, x).double()
+        r, w = ref.decode_tree(x.q, x.k, x.v, x.table, x.seqlens, x.mask, x.counts, x.scale)
+        assert torch.equal(torch.isnan(got), torch.isnan(r)), (where, value)
+        fine = torch.isfinite(r)
+        ref.check(got[fine], r[fine], w[fine])
