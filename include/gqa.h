@@ -460,8 +460,10 @@ GQA_API int gqa_pages_reserve(int32_t *block_table, int32_t *refcount, const int
  * shared prompts): its empty table row lists the same pages up to
  * seqlens[src[i]], each with one more reference, and seqlens[dst[i]] =
  * seqlens[src[i]].  Nothing is copied until gqa_pages_reserve.  A pair is
- * skipped and flags GQA_ERR_PAGES when an index is outside [0, B), a dst row is
- * not empty, is some pair's src or is an earlier pair's dst, or src lacks a page.
+ * skipped and flags GQA_ERR_PAGES when an index is outside [0, B), its dst row is
+ * not empty, is some pair's src or is an earlier pair's dst, its src is some
+ * pair's dst, seqlens[src] is out of range, or src lacks one of its pages or lists
+ * one without references.
  */
 GQA_API int gqa_pages_fork(int32_t *block_table, int32_t *refcount, int32_t *seqlens, const int32_t *src,
                            const int32_t *dst, int n, int B, int page, int num_pages, int M, gqa_stream_t stream);

@@ -247,8 +247,10 @@ __global__ void __launch_bounds__(kPageThreads)
 // seqlens[src[i]] positions of row src[i], each with one more reference.
 // Which pairs run depends on the inputs alone, so the order of the blocks does
 // not matter: a pair is skipped and flagged when an index is out of range, its
-// dst is also some pair's src, an earlier pair has the same dst, dst's row is
-// not empty, or src's table lacks a page.
+// dst is also some pair's src or its src some pair's dst, an earlier pair has the
+// same dst, dst's row is not empty, src's length is out of range, or src's table
+// lacks a page or lists one that nobody holds (with one reference for two rows, a
+// reserve would take the page for either row's own).
 __global__ void __launch_bounds__(kPageThreads)
     pages_fork_kernel(int32_t *table, int32_t *refcount, int32_t *seqlens, const int32_t *src, const int32_t *dst,
                       int n, int B, int M, int page, int P, unsigned *status) {
@@ -256,31 +258,30 @@ __global__ void __launch_bounds__(kPageThreads)
     const int i = blockIdx.x;
     const int a = src[i], z = dst[i];
     bool ok = a >= 0 && a < B && z >= 0 && z < B;
+    int T = 0;
+    if (ok) {
+        // (what a row that another pair writes holds here does not matter: this pair is skipped below)
+        T = seqlens[a];
+#pragma unroll 4
+        for (int k = threadIdx.x; k < M; k += blockDim.x) {  // (no branches: the loads of a round go out together)
+            const int old = table[(size_t)z * M + k], e = table[(size_t)a * M + k];
+            const int held = e >= 0 && e < P ? refcount[e] : 0;  // (counts only rise in this kernel)
+            ok &= old < 0 && ((long long)k * page >= T || held > 0);
+        }
+        ok = ok && T >= 0 && T <= (long long)M * page;
+    }
     for (int k = threadIdx.x; k < n; k += blockDim.x) {
         const int zk = dst[k];
         ok = ok && zk != a && src[k] != z && (k >= i || zk != z);
     }
-    int T = 0, need = 0;
     if (__syncthreads_and(ok)) {
-        T = seqlens[a];
-        ok = T >= 0 && T <= (long long)M * page;
-        need = ok ? (int)(((long long)T + page - 1) / page) : 0;
-        for (int k = threadIdx.x; k < M; k += blockDim.x) {
-            ok = ok && table[(size_t)z * M + k] < 0;
-            if (k < need) {
-                const int e = table[(size_t)a * M + k];
-                ok = ok && e >= 0 && e < P;
-            }
+        for (int k = threadIdx.x; (long long)k * page < T; k += blockDim.x) {
+            const int e = table[(size_t)a * M + k];
+            table[(size_t)z * M + k] = e;
+            atomicAdd(&refcount[e], 1);
         }
-        if (__syncthreads_and(ok)) {
-            for (int k = threadIdx.x; k < need; k += blockDim.x) {
-                const int e = table[(size_t)a * M + k];
-                table[(size_t)z * M + k] = e;
-                atomicAdd(&refcount[e], 1);
-            }
-            if (threadIdx.x == 0) seqlens[z] = T;
-            return;
-        }
+        if (threadIdx.x == 0) seqlens[z] = T;
+        return;
     }
     if (threadIdx.x == 0) set_status(status, STATUS_PAGES);
 }

@@ -366,3 +366,21 @@ def test_append_offsets_that_fall(gqa, page, cu, lens):
         if bad:
             expect(gqa, -7)
         gqa.get_status()
+
+
+def test_fork_of_a_page_that_nobody_holds(gqa):
+    """Row 1 lists a page whose count is 0: its pair is skipped and flagged, the others run, and no page
+    ends with fewer references than rows that list it."""
+    x = Both(gqa, 7, [40, 40, 17], 16, 4, 30, seed=10)
+    lost = x.want.table[1][2]
+    x.ref[lost] = 0
+    before = x.table.clone()
+    counts = x.ref.clone()
+    gqa.pages_fork(x.table, x.ref, x.T, i32([0, 1, 1, 2]), i32([3, 4, 5, 6]), page_size=16)
+    expect(gqa, -9)
+    for a, z in ((0, 3), (2, 6)):
+        held = -(-x.want.T[a] // 16)
+        before[z, :held] = before[a, :held]
+        counts[before[a, :held].long()] += 1
+        x.want.T[z] = x.want.T[a]
+    assert torch.equal(x.table, before) and torch.equal(x.ref, counts) and x.T.tolist() == x.want.T
