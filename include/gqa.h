@@ -371,6 +371,8 @@ GQA_API int gqa_prefill_packed(const void *q, const void *k, const void *v, cons
  * Reference counts [P] int32 say how many table rows list a page; 0 is free.
  * An entry outside [0, num_pages) is never followed; where a call needs one it
  * flags GQA_ERR_PAGES.
+ * What a pool call writes (table, counts, lengths, pools, workspace) must not
+ * overlap its other tensors.
  *
  * gqa_decode_tree -- attention of a tree of drafted tokens over a cache.
  * Sequence b has T_b = seqlens[b] cached positions, followed in the cache by the
@@ -379,13 +381,14 @@ GQA_API int gqa_prefill_packed(const void *q, const void *k, const void *v, cons
  * set (its ancestors and itself):
  *     out[b,i,h,:] = sum_t softmax_t(scale <q[b,i,h], K[b,g,t]>) V[b,g,t,:]
  * over those t.  With one draft this is a single-token step over pages.
- *   q, out      device, [B, n, H, d_h] bf16, 16-byte aligned, not overlapping
+ *   q, out      device, [B, n, H, d_h] bf16, 16-byte aligned
  *   k_cache, v_cache  device, pools or dense caches, bf16, 16-byte aligned
  *   seqlens     device, [B] int32; T_b + n_draft[b] must not exceed the capacity
  *   tree_mask   device, [B, n] int64 bit masks, or NULL: draft i sees drafts j <= i
  *   n_draft     device, [B] int32, 0 <= n_draft[b] <= n, or NULL: n for all
  *   workspace   >= gqa_decode_tree_workspace_bytes(...), 256-byte aligned; its
  *               contents need no initialisation and nothing in it is kept
+ * out and the workspace must not overlap each other or an input.
  * Rows out[b, i >= n_draft[b]] are left as they were.  A row that sees nothing
  * is zero, one that sees a score that is NaN or +inf is NaN.  Positions past
  * T_b + n_draft[b], and drafts that no mask of the sequence names, are never
@@ -412,8 +415,8 @@ GQA_API int gqa_decode_tree(const void *q, const void *k_cache, const void *v_ca
  * page is missing are not written (their number counts all the same) and flag
  * GQA_ERR_PAGES.  Pages that several rows share must be made the writer's own
  * first (gqa_pages_reserve).
- * N >= 1; seqlens_out must not overlap seqlens or cu_seqlens, nor the caches one
- * another or the new rows.  bf16 or fp32, d_h 64 or 128, any page.
+ * N >= 1; seqlens_out and the caches must not overlap one another or an input.
+ * bf16 or fp32, d_h 64 or 128, any page.
  */
 GQA_API int gqa_cache_append(const void *k_new, const void *v_new, const int32_t *cu_seqlens, const int32_t *seqlens,
                              int32_t *seqlens_out, void *k_cache, void *v_cache, const int32_t *block_table, int B,
@@ -429,8 +432,8 @@ GQA_API int gqa_cache_append(const void *k_new, const void *v_new, const int32_t
  * Entries lie in [0, 64); n_keep [B] int32 in [0, m], or NULL: m for all.  A
  * sequence with an entry, count or position out of range (GQA_ERR_SEQLEN) or a
  * page missing (GQA_ERR_PAGES) is left as it was.  The rows written must lie in
- * pages of the sequence's own.  1 <= m <= 64.  seqlens_out must not overlap
- * seqlens.  bf16 or fp32, d_h 64 or 128, any page.
+ * pages of the sequence's own.  1 <= m <= 64.  seqlens_out and the caches must
+ * not overlap one another or an input.  bf16 or fp32, d_h 64 or 128, any page.
  */
 GQA_API int gqa_cache_compact(void *k_cache, void *v_cache, const int32_t *block_table, const int32_t *seqlens,
                               const int32_t *keep, const int32_t *n_keep, int32_t *seqlens_out, int B, int m, int G,

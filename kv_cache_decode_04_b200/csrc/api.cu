@@ -11,6 +11,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 #include <random>
 
@@ -570,6 +571,22 @@ static bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+struct Range {
+    const void *p;  // null: an optional tensor that is not there
+    size_t n;
+};
+
+// Whether no written range overlaps another written one or a read one.
+static bool apart(std::initializer_list<Range> written, std::initializer_list<Range> read) {
+    for (const Range *w = written.begin(); w != written.end(); ++w) {
+        for (const Range *o = w + 1; o != written.end(); ++o)
+            if (w->p && o->p && overlaps(w->p, w->n, o->p, o->n)) return false;
+        for (const Range &o : read)
+            if (w->p && o.p && overlaps(w->p, w->n, o.p, o.n)) return false;
+    }
+    return true;
+}
+
 // Packed query rows [N, H, d_h]: boxes of 64 dims x the r heads of a group x
 // floor(128 / r) tokens, the rows of one tensor-core tile.
 static int make_tmap_rows(CUtensorMap *m, const void *q, long long N, int H, int G, int d_h) {
@@ -600,8 +617,7 @@ int gqa_prefill_packed(const void *q, const void *k, const void *v, const int32_
     if (((long long)N / (2 * (128 / (H / G))) + B + 1) * G >= (1ll << 30))
         return fail(GQA_ERR_UNSUPPORTED, "too many query tiles for one call");
     const size_t qb = (size_t)N * H * d_h * 2, kb = (size_t)N * G * d_h * 2;
-    if (overlaps(out, qb, q, qb) || overlaps(out, qb, k, kb) || overlaps(out, qb, v, kb) ||
-        overlaps(out, qb, cu_seqlens, (size_t)(B + 1) * 4))
+    if (!apart({{out, qb}}, {{q, qb}, {k, kb}, {v, kb}, {cu_seqlens, (size_t)(B + 1) * 4}}))
         return fail(GQA_ERR_INVALID, "out must not overlap an input");
     DeviceInfo *d = nullptr;
     rc = device_info(&d);
@@ -701,8 +717,10 @@ int gqa_decode_tree(const void *q, const void *k_cache, const void *v_cache, con
     if (misaligned(q, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(out, 16) ||
         misaligned(seqlens, 4) || misaligned(tree_mask, 8) || misaligned(n_draft, 4))
         return fail(GQA_ERR_ALIGN, "q, k_cache, v_cache and out must be 16-byte aligned, tree_mask 8-byte");
-    const size_t qb = (size_t)B * n * H * d_h * 2, cb = cache_bytes(c);
-    if (overlaps(out, qb, q, qb) || overlaps(out, qb, k_cache, cb) || overlaps(out, qb, v_cache, cb))
+    const size_t qb = (size_t)B * n * H * d_h * 2, cb = cache_bytes(c), ib = (size_t)B * 4;
+    const Range rq = {q, qb}, rk = {k_cache, cb}, rv = {v_cache, cb}, rt = {block_table, ib * M}, rs = {seqlens, ib},
+                rm = {tree_mask, ib * 2 * n}, rn = {n_draft, ib};
+    if (!apart({{out, qb}}, {rq, rk, rv, rt, rs, rm, rn}))
         return fail(GQA_ERR_INVALID, "out must not overlap an input");
     DeviceInfo *d = nullptr;
     rc = device_info(&d);
@@ -712,6 +730,8 @@ int gqa_decode_tree(const void *q, const void *k_cache, const void *v_cache, con
         return fail(GQA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                     workspace ? workspace_bytes : (size_t)0);
     if (misaligned(workspace, 256)) return fail(GQA_ERR_ALIGN, "workspace must be 256-byte aligned");
+    if (!apart({{workspace, need}, {out, qb}}, {rq, rk, rv, rt, rs, rm, rn}))
+        return fail(GQA_ERR_INVALID, "workspace must not overlap another tensor");
     // one K/V load is the largest power of two that divides the page, 128 at most; a
     // dense row is one page, and what a load takes beyond it reads as zero
     int box = 128;
@@ -760,13 +780,10 @@ int gqa_cache_append(const void *k_new, const void *v_new, const int32_t *cu_seq
     if (N <= 0) return fail(GQA_ERR_INVALID, "N must be positive");
     if (!k_new || !v_new || !cu_seqlens || !seqlens || !seqlens_out || !k_cache || !v_cache)
         return fail(GQA_ERR_INVALID, "null tensor pointer");
-    if (overlaps(seqlens_out, (size_t)B * 4, seqlens, (size_t)B * 4) ||
-        overlaps(seqlens_out, (size_t)B * 4, cu_seqlens, (size_t)(B + 1) * 4))
-        return fail(GQA_ERR_INVALID, "seqlens_out must not overlap seqlens or cu_seqlens");
-    const size_t nb = (size_t)N * G * c.row16 * 16, cb = cache_bytes(c);
-    if (overlaps(k_cache, cb, v_cache, cb) || overlaps(k_cache, cb, k_new, nb) || overlaps(k_cache, cb, v_new, nb) ||
-        overlaps(v_cache, cb, k_new, nb) || overlaps(v_cache, cb, v_new, nb))
-        return fail(GQA_ERR_INVALID, "the caches must not overlap each other or the new rows");
+    const size_t nb = (size_t)N * G * c.row16 * 16, cb = cache_bytes(c), ib = (size_t)B * 4;
+    if (!apart({{seqlens_out, ib}, {k_cache, cb}, {v_cache, cb}},
+               {{k_new, nb}, {v_new, nb}, {cu_seqlens, ib + 4}, {seqlens, ib}, {block_table, ib * M}}))
+        return fail(GQA_ERR_INVALID, "seqlens_out and the caches must not overlap each other or an input");
     if (misaligned(k_new, 16) || misaligned(v_new, 16) || misaligned(k_cache, 16) || misaligned(v_cache, 16) ||
         misaligned(cu_seqlens, 4) || misaligned(seqlens, 4) || misaligned(seqlens_out, 4))
         return fail(GQA_ERR_ALIGN, "k_new, v_new and the caches must be 16-byte aligned");
@@ -789,12 +806,10 @@ int gqa_cache_compact(void *k_cache, void *v_cache, const int32_t *block_table, 
     if (m <= 0 || m > 64) return fail(GQA_ERR_INVALID, "m=%d entries to keep (1 to 64)", m);
     if (!k_cache || !v_cache || !seqlens || !keep || !seqlens_out)
         return fail(GQA_ERR_INVALID, "null tensor pointer");
-    if (overlaps(seqlens_out, (size_t)B * 4, seqlens, (size_t)B * 4) ||
-        overlaps(seqlens_out, (size_t)B * 4, keep, (size_t)B * m * 4) ||
-        (n_keep && overlaps(seqlens_out, (size_t)B * 4, n_keep, (size_t)B * 4)))
-        return fail(GQA_ERR_INVALID, "seqlens_out must not overlap seqlens, keep or n_keep");
-    if (overlaps(k_cache, cache_bytes(c), v_cache, cache_bytes(c)))
-        return fail(GQA_ERR_INVALID, "the caches must not overlap each other");
+    const size_t cb = cache_bytes(c), ib = (size_t)B * 4;
+    if (!apart({{seqlens_out, ib}, {k_cache, cb}, {v_cache, cb}},
+               {{seqlens, ib}, {keep, ib * m}, {n_keep, ib}, {block_table, ib * M}}))
+        return fail(GQA_ERR_INVALID, "seqlens_out and the caches must not overlap each other or an input");
     if ((long long)B * G * 2 >= (1ll << 31)) return fail(GQA_ERR_UNSUPPORTED, "B*G too large");
     if (misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(seqlens, 4) || misaligned(keep, 4) ||
         misaligned(n_keep, 4) || misaligned(seqlens_out, 4))
@@ -843,8 +858,9 @@ int gqa_pages_reserve(int32_t *block_table, int32_t *refcount, const int32_t *se
         return fail(GQA_ERR_UNSUPPORTED, "B*M must be below 2^31 table entries");
     if ((long long)G * page * c.row16 > INT32_MAX - 256)  // the copy of a page counts its pieces in 32 bits
         return fail(GQA_ERR_UNSUPPORTED, "a page must stay below 2^35 bytes");
-    if (overlaps(k_pages, cache_bytes(c), v_pages, cache_bytes(c)))
-        return fail(GQA_ERR_INVALID, "the pools must not overlap each other");
+    const size_t cb = cache_bytes(c), ib = (size_t)B * 4, pb = (size_t)num_pages * 4;
+    if (!apart({{block_table, ib * M}, {refcount, pb}, {k_pages, cb}, {v_pages, cb}}, {{seqlens, ib}, {n_new, ib}}))
+        return fail(GQA_ERR_INVALID, "the tables, the pools and the lengths must not overlap each other");
     if (misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(seqlens, 4) || misaligned(n_new, 4))
         return fail(GQA_ERR_ALIGN, "the pools must be 16-byte aligned");
     const size_t need = gqa::pages_reserve_workspace(B, num_pages);
@@ -852,6 +868,9 @@ int gqa_pages_reserve(int32_t *block_table, int32_t *refcount, const int32_t *se
         return fail(GQA_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                     workspace ? workspace_bytes : (size_t)0);
     if (misaligned(workspace, 256)) return fail(GQA_ERR_ALIGN, "workspace must be 256-byte aligned");
+    if (!apart({{workspace, need}}, {{block_table, ib * M}, {refcount, pb}, {k_pages, cb}, {v_pages, cb}, {seqlens, ib},
+                                     {n_new, ib}}))
+        return fail(GQA_ERR_INVALID, "workspace must not overlap another tensor");
     DeviceInfo *d = nullptr;
     rc = device_info(&d);
     if (rc) return rc;
@@ -872,6 +891,9 @@ int gqa_pages_fork(int32_t *block_table, int32_t *refcount, int32_t *seqlens, co
     if (!seqlens || !src || !dst) return fail(GQA_ERR_INVALID, "null tensor pointer");
     if (misaligned(seqlens, 4) || misaligned(src, 4) || misaligned(dst, 4))
         return fail(GQA_ERR_ALIGN, "seqlens, src and dst must be 4-byte aligned");
+    if (!apart({{block_table, (size_t)B * M * 4}, {refcount, (size_t)num_pages * 4}, {seqlens, (size_t)B * 4}},
+               {{src, (size_t)n * 4}, {dst, (size_t)n * 4}}))
+        return fail(GQA_ERR_INVALID, "block_table, refcount and seqlens must not overlap each other, src or dst");
     DeviceInfo *d = nullptr;
     rc = device_info(&d);
     if (rc) return rc;
@@ -888,6 +910,8 @@ int gqa_pages_release(int32_t *block_table, int32_t *refcount, const int32_t *le
     if (rc) return rc;
     if (!lengths) return fail(GQA_ERR_INVALID, "null tensor pointer");
     if (misaligned(lengths, 4)) return fail(GQA_ERR_ALIGN, "lengths must be 4-byte aligned");
+    if (!apart({{block_table, (size_t)B * M * 4}, {refcount, (size_t)num_pages * 4}}, {{lengths, (size_t)B * 4}}))
+        return fail(GQA_ERR_INVALID, "lengths must not overlap block_table or refcount");
     DeviceInfo *d = nullptr;
     rc = device_info(&d);
     if (rc) return rc;

@@ -281,3 +281,18 @@ def test_a_row_that_sees_a_score_that_is_not_finite_says_so(gqa, n, H, G, T, at)
         assert torch.equal(torch.isnan(got), torch.isnan(r)), (where, value)
         fine = torch.isfinite(r)
         ref.check(got[fine], r[fine], w[fine])
+
+
+def test_a_workspace_that_overlaps_is_refused(gqa):
+    x = Case(2, 4, 4, 2, 64, 16, [5, 40], seed=33)
+    a, kw = x.args()
+    size = gqa.decode_tree_workspace_bytes(2, 4, 4, 2, 64)
+    out = torch.empty(x.q.numel() * 2 + size, dtype=torch.uint8, device="cuda")
+    rows = out[:x.q.numel() * 2].view(torch.bfloat16).view(x.q.shape)
+    gqa.decode_tree(*a, out=rows, workspace=out[x.q.numel() * 2:], **kw)
+    want = rows.clone()
+    with pytest.raises(gqa.GQAError) as e:
+        gqa.decode_tree(*a, out=rows, workspace=out[x.q.numel() * 2 - 256:], **kw)
+    assert e.value.code == -1
+    gqa.get_status()
+    assert torch.equal(rows, want)

@@ -150,3 +150,29 @@ def test_pages_reserve_table_of_2g_entries():
     assert reserve(8192, 1 << 18, 1) == -2
     assert reserve(8192, (1 << 18) - 1, 1) == -5  # only the workspace is missing
     assert reserve(1, 134217711) == -5
+
+
+def test_what_is_written_overlaps_nothing():
+    """Each call with one tensor at the beginning or end of one that it writes."""
+    ints = 2 * 5 * 4                       # block_table [2, 5]
+    rows = 2 * 4 * 8 * 64 * 2              # q, out [2, 4, 8, 64] bf16
+    pool = 10 * 2 * 16 * 64 * 2            # [10, 2, 16, 64] bf16
+    for name in ("table", "sl", "mask", "nd"):
+        assert tree(**{name: G_ + rows - 8}) == -1, name
+    dense = 2 * 2 * 100 * 64 * 4           # [2, 2, 100, 64] fp32
+    for kw in (dict(cu=F + dense - 4), dict(sl=G_ + dense - 4), dict(slo=F + dense - 8), dict(slo=A), dict(slo=C + 8)):
+        assert append(**kw) == -1, kw
+    assert append(table=E, M=5) == -1 and append(table=F, M=5) == -1
+    for kw in (dict(sl=A + 16), dict(keep=BB), dict(nk=A), dict(table=G_), dict(slo=A + 64), dict(table=BB)):
+        assert compact(**kw) == -1, kw
+
+    def reserve(t=A, r=BB, sl=C, n=D, k=E, v=F, ws=G_):
+        return L.gqa_pages_reserve(t, r, sl, n, k, v, 2, 2, 64, 16, 10, 5, gqa.GQA_BF16, ws, 1 << 20, None)
+
+    for kw in (dict(sl=A + ints - 4), dict(n=BB + 36), dict(t=E + pool - 32), dict(r=F), dict(sl=E), dict(ws=A),
+               dict(ws=BB), dict(ws=C), dict(ws=D), dict(ws=E + pool - 256), dict(ws=F)):
+        assert reserve(**kw) == -1, kw
+    for args in ((A, BB, A + ints - 4, D, E), (A, BB, BB, D, E), (A, BB, C, A, E), (A, BB, C, D, BB + 36), (A, BB, C, C, E)):
+        assert L.gqa_pages_fork(*args, 2, 2, 16, 10, 5, None) == -1, args
+    for lengths in (A + ints - 4, BB):
+        assert L.gqa_pages_release(A, BB, lengths, 2, 16, 10, 5, None) == -1
