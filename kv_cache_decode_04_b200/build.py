@@ -1,4 +1,4 @@
-"""Builds libgqa.so in-tree with nvcc for sm_100a, and the binding's C part _binding.so with the C
+"""Builds libgqa.so in-tree with nvcc for sm_100a, and the binding's C part _binding with the C
 compiler (no torch in either link)."""
 from __future__ import annotations
 
@@ -15,8 +15,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgqa.so")
 # the same library with the device-side index checks compiled in (-DGQA_DEBUG)
 LIB_DEBUG = os.path.join(PKG, "libgqa_debug.so")
-# the CPython side of the short calls
-BINDING = os.path.join(PKG, "_binding.so")
+# the CPython side of the short calls, named for the interpreter that it is built for: another
+# one does not load it
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 BINDING_SRC = os.path.join(CSRC, "binding.c")
 
 NVCC_FLAGS = [
@@ -59,7 +60,10 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """Compiles _binding.so unless it is newer than its source and the header."""
+    """Compiles _binding unless it is newer than its source and the header."""
+    plain = os.path.join(PKG, "_binding.so")  # the name that any interpreter would load
+    if os.path.exists(plain) and plain != BINDING:
+        os.remove(plain)
     deps = [BINDING_SRC, os.path.join(INCLUDE, "gqa.h")]
     if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
         return BINDING

@@ -105,3 +105,12 @@ def test_projections_reject_bad_arguments_on_host():
     # the layer step needs the post-append lengths
     assert L.gqa_layer_decode_step(x, w, w, w, w, o, o, x, None, 0.1, 0, o, 4, 256, 8, 2, 128, 16,
                                    gqa.GQA_BF16, None, 0, None) == -1
+
+
+def test_the_binding_module_is_the_interpreters_own():
+    """Another Python version does not load a module that was built for this one."""
+    import sysconfig
+
+    path = gqa._binding.__file__
+    assert path.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert not os.path.exists(os.path.join(os.path.dirname(path), "_binding.so"))
