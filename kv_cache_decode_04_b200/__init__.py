@@ -500,7 +500,8 @@ def decode_tree_workspace_bytes(B, n, H, G, d_h) -> int:
 
 @functools.lru_cache(maxsize=256)
 def _tree_workspace(index, B, n, H, G, d_h):
-    return decode_tree_workspace_bytes(B, n, H, G, d_h)
+    with torch.cuda.device(index):  # the size goes by that device's SMs, whichever is current
+        return decode_tree_workspace_bytes(B, n, H, G, d_h)
 
 
 def decode_tree(q, k_cache, v_cache, seqlens, tree_mask=None, n_draft=None, block_table=None, scale=None, out=None,

@@ -176,3 +176,23 @@ def test_what_is_written_overlaps_nothing():
         assert L.gqa_pages_fork(*args, 2, 2, 16, 10, 5, None) == -1, args
     for lengths in (A + ints - 4, BB):
         assert L.gqa_pages_release(A, BB, lengths, 2, 16, 10, 5, None) == -1
+
+
+def test_the_tree_workspace_is_sized_for_the_tensors_device(monkeypatch):
+    """Its size is kept by device and shape: it is asked of that device, not of the current one."""
+    import contextlib
+
+    current = [0]
+
+    @contextlib.contextmanager
+    def device(index):
+        was, current[0] = current[0], index
+        yield
+        current[0] = was
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(gqa, "decode_tree_workspace_bytes", lambda *shape: 1000 + current[0])
+    gqa._tree_workspace.cache_clear()
+    assert gqa._tree_workspace(5, 1, 2, 4, 2, 64) == 1005
+    assert gqa._tree_workspace(0, 1, 2, 4, 2, 64) == 1000
+    gqa._tree_workspace.cache_clear()
