@@ -445,7 +445,9 @@ GQA_API int gqa_cache_compact(void *k_cache, void *v_cache, const int32_t *block
  * a page that other rows share is replaced by a free one (copy-on-write: the
  * rows below seqlens[b] are copied, the shared page loses a reference).  Which
  * entries need a page is decided on the counts before the call, and the lowest
- * free pages are handed out in table order, so the result is deterministic.
+ * free pages are handed out in table order, so the result is deterministic.  (When
+ * every row that shares a page reserves it in one call, each gets a copy and the
+ * page itself becomes free: the call needs one page more than the rows do.)
  * All or nothing: with too few free pages nothing changes and GQA_ERR_PAGES is
  * flagged.  A sequence whose range is negative or beyond its capacity is
  * skipped and flags GQA_ERR_SEQLEN.

@@ -34,8 +34,9 @@
 //
 // What bounds it (d_h = 128): one key tile of two row tiles is 2,048 cycles of
 // tensor time and takes 3,990, two groups of 16 MMAs at 80-125 cycles each
-// beside the other row tile's softmax: 975 TFLOP/s on 2 x 8192 tokens and 64
-// heads, the rate of prefill.cu.  With one row tile the two parities overlap and
+// beside the other row tile's softmax: 970-973 TFLOP/s on 2 x 8192 tokens and 64
+// heads under the power cap (1,113 before it), where prefill.cu has 965-967
+// (1,095).  With one row tile the two parities overlap and
 // a tile takes the 2,430 cycles that HBM needs for its 64 KB (7.4 TB/s).
 #pragma once
 

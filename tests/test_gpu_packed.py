@@ -258,3 +258,9 @@ def test_a_row_that_sees_a_value_that_is_not_finite_says_so(gqa, where, value, H
     fine = torch.isfinite(r) & torch.isfinite(got)
     assert fine.sum() > 0.4 * r.numel() and torch.equal(torch.isfinite(got), torch.isfinite(r))
     ref.check(got[fine], r[fine], w[fine])
+
+
+def test_no_tokens_at_all(gqa):
+    for cu in ([0, 0], [3, 3, 3], [0] * 2000):
+        q, k, v = inputs([0, 3], 4, 2, 64, seed=17)
+        assert (run(gqa, q, k, v, cu) == 7.0).all()

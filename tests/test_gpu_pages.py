@@ -384,3 +384,13 @@ def test_fork_of_a_page_that_nobody_holds(gqa):
         counts[before[a, :held].long()] += 1
         x.want.T[z] = x.want.T[a]
     assert torch.equal(x.table, before) and torch.equal(x.ref, counts) and x.T.tolist() == x.want.T
+
+
+def test_append_of_no_rows(gqa):
+    k, v, table = caches(3, 2, 64, 16, 64, torch.bfloat16, seed=6)
+    kn = torch.ones((5, 2, 64), dtype=torch.bfloat16)
+    kd, vd = k.cuda(), v.cuda()
+    for cu in ([0, 0, 0, 0], [5, 5, 5, 5], [2, 2, 2, 2]):
+        got = gqa.cache_append(kn.cuda(), kn.cuda(), i32(cu), i32([0, 64, 7]), kd, vd, block_table=table.cuda())
+        assert got.tolist() == [0, 64, 7] and same(kd, k) and same(vd, v)
+    gqa.get_status()
