@@ -394,3 +394,69 @@ def test_append_of_no_rows(gqa):
         got = gqa.cache_append(kn.cuda(), kn.cuda(), i32(cu), i32([0, 64, 7]), kd, vd, block_table=table.cuda())
         assert got.tolist() == [0, 64, 7] and same(kd, k) and same(vd, v)
     gqa.get_status()
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_rows_on_another_stream_and_replayed(gqa, page):
+    """Append and compact queued on a side stream, with lengths that they allocate, and captured: each
+    replay takes the lengths that it finds."""
+    B, G, d = 3, 2, 64
+    k, v, table = caches(B, G, d, page, 96, torch.bfloat16, seed=11)
+    gen = torch.Generator().manual_seed(12)
+    kn, vn = (torch.randn((12, G, d), generator=gen).to(torch.bfloat16) for _ in range(2))
+    cu, lens, keep, n_keep = [0, 5, 6, 12], [3, 40, 15], [[0, 2, 4], [0, 0, 0], [5, 1, 3]], [3, 1, 2]
+    bt = None if table is None else table.cuda()
+    args = kn.cuda(), vn.cuda(), i32(cu)
+    T, kp, nk = i32(lens), i32(keep), i32(n_keep)
+
+    def step(kd, vd, T, stream=None):
+        gqa.cache_append(*args, T, kd, vd, block_table=bt, stream=stream)
+        return gqa.cache_compact(kd, vd, T, kp, n_keep=nk, block_table=bt, stream=stream)
+
+    def model(T):
+        for b in range(B):
+            for i in range(cu[b + 1] - cu[b]):
+                p, r = ref.place(table, page, b, T[b] + i)
+                k[p, :, r], v[p, :, r] = kn[cu[b] + i], vn[cu[b] + i]
+            rows = [ref.place(table, page, b, T[b] + j) for j in keep[b][:n_keep[b]]]
+            was = [(k[p, :, r].clone(), v[p, :, r].clone()) for p, r in rows]
+            for j, (x, y) in enumerate(was):
+                p, r = ref.place(table, page, b, T[b] + j)
+                k[p, :, r], v[p, :, r] = x, y
+        return [t + c for t, c in zip(T, n_keep)]
+
+    kd, vd = k.cuda(), v.cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = step(kd, vd, T, side)
+    side.synchronize()
+    lens = model(lens)
+    assert got.tolist() == lens and same(kd, k) and same(vd, v)
+    T.copy_(got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(kd, vd, T)
+    for _ in range(4):
+        graph.replay()
+        T.copy_(got)
+        lens = model(lens)
+        assert T.tolist() == lens and same(kd, k) and same(vd, v)
+    gqa.get_status()
+
+
+def test_pool_calls_on_another_stream(gqa):
+    x = Both(gqa, 4, [21, 40], 16, 6, 40, seed=13)
+    side = torch.cuda.Stream()
+    hold, src, dst, new = i32([21, 33, 0, 0]), i32([0, 1]), i32([2, 3]), i32([1, 2, 3, 20])
+    side.wait_stream(torch.cuda.current_stream())
+    gqa.pages_release(x.table, x.ref, hold, page_size=16, stream=side)
+    gqa.pages_fork(x.table, x.ref, x.T, src, dst, page_size=16, stream=side)
+    gqa.pages_reserve(x.table, x.ref, x.T, new, x.kd, x.vd, stream=side)
+    side.synchronize()
+    x.want.release([21, 33, 0, 0])
+    x.want.fork([0, 1], [2, 3])
+    x.want.reserve([1, 2, 3, 20])
+    for e, p, rows in x.want.copies:
+        x.k[p, :, :rows], x.v[p, :, :rows] = x.k[e, :, :rows], x.v[e, :, :rows]
+    x.check()
+    gqa.get_status()
